@@ -9,6 +9,10 @@ works but every call raises.
     h = Handle()
     h.run(A, B, C, quant="fp8_dynamic", act="none", sa=sa, sb=sb, bias=bias)
 
+The operators between the layers when tokens are served (norms and rotation
+of heads, a paged cache, attention over it, log probabilities) are methods of
+the same handle, in ``epilogue_scaled_gemm_amd.serving``.
+
 PyTorch integration (custom operators with fake implementations, an FX pass
 that fuses linear + epilogue chains) lives in ``epilogue_scaled_gemm_amd.torch_ops``.
 
@@ -22,6 +26,9 @@ import os
 
 import torch
 
+from . import serving
+from .serving import node_slots, rope_table, tree_mask  # noqa: F401
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "liblingemm.so")
 
@@ -34,7 +41,9 @@ STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported", -3: "HIP error",
 EXPORTS = ("lin_gemm_create", "lin_gemm_run", "lin_gemm_destroy", "lin_gemm_strerror",
            "lin_gemm_last_error", "lin_gemm_set_force", "lin_gemm_describe",
            "lin_gemm_run_unfused", "lin_gemm_quantize", "lin_gemm_run_dynamic",
-           "lin_gemm_run_grouped", "lin_gemm_run_noalloc", "lin_gemm_stream_read")
+           "lin_gemm_run_grouped", "lin_gemm_run_noalloc", "lin_gemm_stream_read",
+           "lin_gemm_qk_norm_rope", "lin_gemm_kv_append", "lin_gemm_tree_attention",
+           "lin_gemm_token_logprobs")
 DQ_KIND = {"fp8_token": 0, "int8_token": 1, "fp8_block": 2}
 X_DTYPE = {"bf16": 0, "fp16": 1}
 
@@ -91,6 +100,7 @@ def library():
     lib.lin_gemm_run_grouped.argtypes = [P, P, P, ctypes.POINTER(_Scales), P, P, P, P, I64, I64,
                                          I64, I64, I64, I, I, P]
     lib.lin_gemm_run_grouped.restype = I
+    serving.declare(lib)
     _lib = lib
     return lib
 
@@ -157,8 +167,9 @@ def _check_layer(quant, act, M, N, K, A=None, B=None, C=None, sa=None, sb=None, 
         _need("sb (E8M0 bytes)", sb, N * (K // 32), 1)
 
 
-class Handle:
-    """One lin_gemm handle (variant table + split-K workspace)."""
+class Handle(serving.ServingOps):
+    """One lin_gemm handle (variant table + split-K workspace); the operators
+    between the linear layers are in ``serving``."""
 
     def __init__(self, config_path=None):
         self._lib = library()

@@ -18,7 +18,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["kernels_tile.hip", "kernels_pp.hip", "kernels_decode.hip", "kernels_misc.hip",
-           "kernels_quant.hip", "dispatch.cpp", "abi.cpp"]
+           "kernels_quant.hip", "kernels_rope.hip", "kernels_attn.hip", "kernels_score.hip",
+           "dispatch.cpp", "abi.cpp", "abi_serving.cpp"]
 
 # Packed fp32 instructions are disabled for all device code.
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall", "-Wno-unused-result",

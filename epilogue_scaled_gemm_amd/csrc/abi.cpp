@@ -21,43 +21,15 @@
 
 #include "../../include/lin_gemm.h"
 #include "dispatch.hpp"
+#include "handle.hpp"
 #include "launch.hpp"
 
-struct lin_gemm_ctx {
-  std::vector<lg::TableEntry> table;
-  bool forced = false;
-  lg::Variant force;
-  std::string last_error;
-  void* ws = nullptr;         // split-K workspace
-  size_t ws_bytes = 0;
-  int* counters = nullptr;    // per-16-row-group arrival counters (kept at zero between calls)
-  size_t counters_n = 0;
-  void* dq = nullptr;         // staging of lin_gemm_run_dynamic: codes, then scales
-  size_t dq_bytes = 0;
-  // Buffers replaced by bigger ones.  They stay allocated until the handle
-  // is destroyed: a graph captured before the growth still holds their
-  // addresses and may be replayed.
-  std::vector<void*> retired;
-};
+using lg::fail;
+using lg::grow_size;
+using lg::hip_fail;
+using lg::misaligned;
 
 namespace {
-
-int fail(lin_gemm_t h, int status, const std::string& msg) {
-  if (h) h->last_error = msg;
-  return status;
-}
-
-int hip_fail(lin_gemm_t h, hipError_t e, const char* what) {
-  return fail(h, LIN_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
-}
-
-// Sizes of handle-owned buffers grow in powers of two (at least 1 MiB), so
-// the retired ones add up to less than the live one.
-size_t grow_size(size_t need) {
-  size_t b = (size_t)1 << 20;
-  while (b < need) b <<= 1;
-  return b;
-}
 
 // Bytes per element of A (bf16 activations in the MXFP4 mode).
 int esize(int quant) {
@@ -80,8 +52,6 @@ int qkind(int quant) {
 int64_t b_row_bytes(int quant, int64_t K) {
   return quant == LIN_Q_MXFP4 ? K / 2 : K * esize(quant);
 }
-
-bool misaligned(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 
 // Shape / pointer checks shared by the fused and unfused entry points.
 int check_shape(lin_gemm_t h, int quant, int64_t M, int64_t N, int64_t K) {

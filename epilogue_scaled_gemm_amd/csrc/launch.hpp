@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "device_common.hpp"
 
 namespace lg {
@@ -139,5 +141,75 @@ hipError_t launch_stream_read(const void* src, int64_t bytes, int grid, int unro
 enum DQKind : int { DQ_FP8_TOKEN = 0, DQ_INT8_TOKEN = 1, DQ_FP8_BLOCK = 2 };
 hipError_t launch_dynamic_quant(int kind, bool f16, const void* X, int64_t M, int64_t K, void* Q,
                                 float* scales, hipStream_t s);
+
+// ------------------------------------------------------- serving operators
+//
+// Between the linear layers of a decoder (kernels_rope.hip, kernels_attn.hip,
+// kernels_score.hip).  Strides are in elements.
+
+// A head tensor [T][H][D] (token and head strides) or a cache
+// [pages][H][page][D] (page, head and in-page token strides).
+struct HeadView {
+  void* p;
+  int64_t ps, ts, hs;
+};
+struct HeadArgs {
+  HeadView q, k, v, q_out, k_out, kc, vc;
+  const uint16_t *q_weight, *k_weight;  // [D] or null: no norm
+  const float* table;                   // [max_pos][rot]: cos, then sin; null: no rotation
+  const int* positions;                 // [T]
+  const int* slots;                     // [T]; null: no cache, keys go to k_out
+  const float *k_scale, *v_scale;       // [Hk] or null (e4m3 cache)
+  int64_t capacity;                     // slots of the cache
+  int page_log;
+  int Hq, Hk, Hv, D, rot, max_pos;
+  float eps;
+  int interleaved, cache8;
+};
+hipError_t launch_heads(const HeadArgs& a, int64_t T, bool f16, hipStream_t s);
+
+struct AttnArgs {
+  const uint16_t* q;
+  const void *k, *v;
+  uint16_t* out;           // [T][Hq][D]
+  float* lse;              // [T][Hq] or null
+  const int *table, *context, *offsets;
+  const int64_t* mask;     // [T][mask_words] or null: nodes see the nodes before them
+  const float *k_scale, *v_scale;
+  float* part_o;           // [nsplit][rows][D]
+  float* part_ml;          // [nsplit][rows][2]
+  int* nsp;                // [rows]
+  int64_t q_ts, q_hs, k_ps, k_hs, k_ts, v_ps, v_hs, v_ts;
+  int64_t T, rows, table_stride;
+  int Hk, G, mask_words, max_pages, pages, page_log, page_mask;
+  int nwork, ntiles, nsplit, chunk;
+  float scale_log2e;
+};
+// How a call is cut: rw row tiles of 32 per workgroup, ntiles workgroups over
+// a sequence's rows, nsplit splits of `chunk` positions.
+struct AttnPlan {
+  int rw;
+  int64_t ntiles, nsplit, chunk;
+};
+AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len);
+// D is 64, 128 or 256.
+hipError_t launch_attention(const AttnArgs& a, int D, int rw, bool f16, bool kv8, hipStream_t s);
+
+struct ScoreArgs {
+  const void* logits;
+  const int* tokens;
+  float *logprobs, *entropy;
+  int* top_ids;
+  float* top_logprobs;
+  float* part_sums;        // [T][nsplit][3]
+  uint64_t* part_keys;     // [T][nsplit][k]
+  int64_t T, V, stride, slice;
+  int k, nsplit;
+  float c, inv_t;          // log2(e) / temperature, 1 / temperature
+};
+constexpr int SCORE_MAX_TOP = 32;
+// elem: 0 bf16, 1 fp16, 2 fp32.
+void score_plan(int64_t T, int64_t V, int elem, int* nsplit, int64_t* slice);
+hipError_t launch_score(const ScoreArgs& a, int elem, hipStream_t s);
 
 }  // namespace lg

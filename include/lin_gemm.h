@@ -286,6 +286,145 @@ int lin_gemm_run_grouped(lin_gemm_t h, const void *A, const void *B, const lin_s
                          int64_t E, int64_t M, int64_t N, int64_t K, int64_t max_rows,
                          int quant_mode, int activation, void *stream);
 
+/* ------------------------------------------------------ serving operators
+ *
+ * What stands between the linear layers of a decoder when tokens are served:
+ * the QKV product's heads are normalised and rotated, keys and values go to
+ * a paged cache, the new tokens attend over that cache, and the head
+ * product's logits are scored.  "New tokens" are one per sequence in plain
+ * decoding, a tree of drafted tokens when drafts are verified, or a part of
+ * a prompt.  Forward only.  The rules of the calls above hold here too:
+ * argument checks on the host before anything is enqueued, device-side plans
+ * (positions, slots, page tables, lengths, offsets, token ids) read by the
+ * kernels, with out-of-range entries turned into skipped or wrong rows,
+ * never into accesses outside the buffers; enqueued on `stream`, without
+ * waiting.
+ *
+ * Head tensors [tokens][heads][dim] are given by address and by token and
+ * head strides in elements (multiples of 8; dim contiguous; 16-byte aligned),
+ * so the parts of one QKV product need no copy.  A cache is [pages][heads]
+ * [page][dim] with page, head and in-page token strides (multiples of 8, of
+ * 16 for e4m3; any order of the three is a cache), page_size a power of two;
+ * cache slot s is token s % page_size of page s / page_size. */
+enum lin_cache_type {
+    LIN_CACHE_BF16 = 0,
+    LIN_CACHE_FP16 = 1,
+    LIN_CACHE_E4M3 = 2 /* value = code * scale[head], scales fp32 or NULL (1) */
+};
+
+typedef struct {
+    int64_t dtype;     /* LIN_Q_BF16 or LIN_Q_FP16: heads, weights, outputs   */
+    int64_t tokens, dim; /* dim: a multiple of 16 up to 256                   */
+    int64_t q_heads;   /* 0 = no queries in this call                         */
+    const void *q;
+    int64_t q_token_stride, q_head_stride;
+    void *q_out;       /* may be q itself                                     */
+    int64_t q_out_token_stride, q_out_head_stride;
+    int64_t kv_heads;
+    const void *k;
+    int64_t k_token_stride, k_head_stride;
+    void *k_out;       /* lin_gemm_qk_norm_rope only; may be k itself         */
+    int64_t k_out_token_stride, k_out_head_stride;
+    const void *v;     /* lin_gemm_kv_append only, as what follows up to slots */
+    int64_t v_token_stride, v_head_stride;
+    void *k_cache;
+    int64_t k_page_stride, k_cache_head_stride, k_in_page_stride;
+    void *v_cache;
+    int64_t v_page_stride, v_cache_head_stride, v_in_page_stride;
+    int64_t cache_type; /* the dtype's own, or LIN_CACHE_E4M3                 */
+    int64_t pages, page_size;
+    const float *k_scale, *v_scale; /* [kv_heads], e4m3 caches                */
+    const int32_t *slots; /* [tokens]; outside [0, pages * page_size): not stored */
+    const void *q_weight, *k_weight; /* [dim] norm weights, or NULL: no norm  */
+    double eps;
+    const float *rope; /* [rope_rows][rope_dim]: cosines, then sines; or NULL */
+    int64_t rope_rows, rope_dim; /* rope_dim: a multiple of 16 up to dim      */
+    const int32_t *positions; /* [tokens], clamped into [0, rope_rows)        */
+    int64_t interleaved; /* 0: pairs (i, i + rope_dim/2); 1: (2i, 2i + 1)     */
+} lin_heads_t;
+
+/* Norms of queries and keys for each head and the position rotation, one
+ * pass:  y = x / sqrt(mean(x^2) + eps) * w  where w is given, then each pair
+ * (a, b) of the first rope_dim values becomes (a c - b s, b c + a s) with c
+ * and s from the table row of the token's position.  Computed in binary32,
+ * rounded once.  Outputs may be the inputs themselves (same address and
+ * strides), not otherwise overlap them.  kv_heads may be 0. */
+int lin_gemm_qk_norm_rope(lin_gemm_t h, const lin_heads_t *args, void *stream);
+
+/* Append keys and values to a paged cache, with the norm and rotation of
+ * lin_gemm_qk_norm_rope applied to the keys on the way, and, where q_heads >
+ * 0, to the queries in the same launch.  Values are stored unchanged (or as
+ * e4m3 codes: x / scale rounded to nearest even, saturated to +-448; NaN
+ * stays NaN).  Tokens that name one slot twice leave either of the two
+ * there. */
+int lin_gemm_kv_append(lin_gemm_t h, const lin_heads_t *args, void *stream);
+
+typedef struct {
+    int64_t dtype;            /* LIN_Q_BF16 or LIN_Q_FP16: q and out          */
+    int64_t tokens, q_heads, kv_heads, dim; /* dim: 64, 128 or 256            */
+    const void *q;            /* [tokens][q_heads][dim]                       */
+    int64_t q_token_stride, q_head_stride;
+    const void *k_cache;
+    int64_t k_page_stride, k_head_stride, k_in_page_stride;
+    const void *v_cache;
+    int64_t v_page_stride, v_head_stride, v_in_page_stride;
+    int64_t cache_type;       /* the dtype's own, or LIN_CACHE_E4M3           */
+    int64_t pages, page_size;
+    const float *k_scale, *v_scale; /* [kv_heads] or NULL, e4m3 caches        */
+    int64_t sequences;
+    const int32_t *page_table; /* [sequences][table_stride], max_pages used   */
+    int64_t table_stride, max_pages;
+    const int32_t *context;   /* [sequences]: cached tokens before the nodes  */
+    const int32_t *offsets;   /* [sequences + 1]: nodes of sequence b are the
+                                 rows offsets[b] .. offsets[b + 1] of q       */
+    int64_t max_context, max_nodes; /* bounds the caller knows of the two;
+                                 they shape the launch, any lengths are right */
+    const int64_t *mask;      /* [tokens][mask_words] or NULL                 */
+    int64_t mask_words;
+    double scale;             /* of the scores                                */
+    void *out;                /* [tokens][q_heads][dim], contiguous           */
+    float *lse;               /* [tokens][q_heads] or NULL                    */
+} lin_attention_t;
+
+/* Attention of the new tokens ("nodes") of each sequence over its paged
+ * cache, which holds their keys and values too: node j of sequence b at
+ * position context[b] + j.  Every node sees the whole context; of the nodes
+ * it sees node j if bit j % 64 of its mask word j / 64 is set (itself not
+ * unless named, and no node beyond the words), or without a mask itself and
+ * the nodes before it.  q head h uses key head h / (q_heads / kv_heads).
+ * out = softmax(scale q k) v; lse = log of the sum of exp(scale q k).  A row
+ * that sees nothing, or only scores of -inf, gets zeros and an lse of -inf.
+ * Positions a row does not see do not reach it, infinities and NaN there
+ * included.  Scores, sums and lse are binary32; the probabilities are
+ * rounded to dtype for the product with the values.  Positions beyond the
+ * page table are cut off.  Long contexts are split over workgroups, whose
+ * sums go to the handle's workspace (grown on demand: warm a shape up before
+ * capturing it). */
+int lin_gemm_tree_attention(lin_gemm_t h, const lin_attention_t *args, void *stream);
+
+typedef struct {
+    int64_t dtype;            /* 0 bf16, 1 fp16, 2 fp32                       */
+    int64_t rows, vocab;
+    const void *logits;       /* [rows][vocab], row_stride elements apart     */
+    int64_t row_stride;
+    const int32_t *tokens;    /* [rows]                                       */
+    double temperature;       /* > 0                                          */
+    float *logprobs;          /* [rows]                                       */
+    float *entropy;           /* [rows] or NULL                               */
+    int64_t top;              /* 0 .. 32, at most vocab                       */
+    int32_t *top_ids;         /* [rows][top] or NULL                          */
+    float *top_logprobs;      /* [rows][top] or NULL                          */
+} lin_score_t;
+
+/* Log probabilities of given tokens:  z = logits / temperature, logprobs =
+ * z[token] - log sum exp z, entropy = -sum p log p in nats (a probability of
+ * zero adds nothing), and the `top` most likely tokens with their log
+ * probabilities, larger logits first, equal ones by lower index.  Sums are
+ * binary32.  A token outside [0, vocab) has the log probability NaN.  A row
+ * with NaN, with +inf, or with nothing above -inf has NaN probabilities (and
+ * some indices in range).  Rows need no alignment beyond their element's. */
+int lin_gemm_token_logprobs(lin_gemm_t h, const lin_score_t *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
