@@ -245,14 +245,12 @@ int run_attention(lin_gemm_t h, const lin_attention_t* p, hipStream_t s) {
   a.chunk = (int)plan.chunk;
   if (a.nsplit > 1) {
     const size_t n = (size_t)a.nsplit * (size_t)a.rows;
-    const size_t counts = ((size_t)a.rows * sizeof(int) + 255) & ~(size_t)255;
-    rc = ensure_bytes(h, counts + n * (size_t)(p->dim + 2) * sizeof(float), s);
+    rc = ensure_bytes(h, n * (size_t)(p->dim + 2) * sizeof(float), s);
     if (rc != LIN_OK) return rc;
-    a.nsp = (int*)h->ws;
-    a.part_o = (float*)((char*)h->ws + counts);
+    a.part_o = (float*)h->ws;
     a.part_ml = a.part_o + n * (size_t)p->dim;
   }
-  hipError_t e = lg::launch_attention(a, (int)p->dim, plan.rw, p->dtype == LIN_Q_FP16, kv8, s);
+  hipError_t e = lg::launch_attention(a, (int)p->dim, plan.shape, p->dtype == LIN_Q_FP16, kv8, s);
   return e == hipSuccess ? LIN_OK : hip_fail(h, e, "attention launch");
 }
 

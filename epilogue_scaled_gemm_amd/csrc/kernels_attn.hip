@@ -10,20 +10,24 @@
 // weighted value sum O (exp2 of scores that carry log2 e):
 //   m' = max(m, s),  l' = l 2^(m - m') + sum 2^(s - m'),  O likewise.
 //
-// Layout.  The rows of one key head (its nodes times the query heads that
-// share it) are packed into tiles of 32 per wave, so a key is read once for
-// all heads of a group.  Scores are formed transposed, S^T = K Q^T, with
-// the 32x32x16 MFMA: a lane then holds 16 scores of ONE row, so the row
-// statistics are register reductions and one half-wave swap, and the
-// rounded probabilities are already the B operand of O^T = V^T P^T -- the
-// contraction order over positions is permuted the same way on the V side,
-// whose fragments come from LDS by transposing reads.
+// Scores are formed transposed, S^T = K Q^T, by MFMA: a lane then holds
+// scores of ONE row, so the row statistics are register reductions and a few
+// lane swaps, and the rounded probabilities are already the B operand of
+// O^T = V^T P^T -- the contraction order over positions is permuted the same
+// way on the V side, whose fragments come from LDS by transposing reads.  The
+// rows of one key head (its nodes times the query heads that share it) are
+// packed into one tile, so a key is read once for all heads of a group.
 //
-// Four waves of a workgroup share each tile of keys and values in LDS.  They
-// are arranged as RW row tiles x CW shares of the positions: few rows split
-// the positions (1 x 4), many rows split the rows (4 x 1).  Long contexts
-// are split over workgroups too; those write (m, l, O) in 32 bits and a
-// second kernel joins them.
+// Two kernels, by the number of those rows:
+//  - stream_kernel (few rows: decode steps and small trees; bound by reading
+//    the cache): every wave runs through positions of its own, 32 at a time,
+//    without barriers: keys go from memory straight into MFMA operands,
+//    values through the wave's own LDS.
+//  - tile_kernel (many rows: large trees, parts of prompts; bound by the
+//    matrix units): 32 rows per wave, all waves share each tile of
+//    positions in LDS, double-buffered.
+// Long contexts are split over workgroups; those write (m, l, O) in 32 bits
+// and join_kernel joins them.
 #include "launch.hpp"
 
 namespace lg {
@@ -34,7 +38,8 @@ typedef __attribute__((ext_vector_type(4))) short s16x4;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) char lds_char;
 
-constexpr int AT_THREADS = 256;
+typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+
 constexpr float NEG_INF = -__builtin_inff();
 
 __device__ inline float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -82,10 +87,439 @@ template <bool F16> __device__ inline bool not_finite2(int w) {
   return (w & E) == E || ((w >> 16) & E) == E;
 }
 
-// ------------------------------------------------------------ LDS tiles
-// A tile holds its rows as 16-byte chunks (8 values); the chunk index is
-// XOR-ed with the row so that 32 lanes that read one chunk of 32 rows (K) or
-// four rows of two chunks (V, transposing reads) use all banks.
+// Maximum / sum of the four lanes l, l ^ 16, l ^ 32, l ^ 48.
+__device__ inline float quad_max(float x) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ inline float quad_sum(float x) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
+template <bool F16> __device__ inline f32x4 mfma16(i32x4 a, i32x4 b, f32x4 c) {
+  if constexpr (F16) return Mfma<QK_FP16>::mma(a, b, c);
+  else return Mfma<QK_BF16>::mma(a, b, c);
+}
+
+// Eight e4m3 codes -> eight 16-bit floats.
+template <bool F16> __device__ inline i32x4 widen8(int lo, int hi) {
+  return i32x4{widen2<F16, false>(lo), widen2<F16, true>(lo), widen2<F16, false>(hi),
+               widen2<F16, true>(hi)};
+}
+
+template <bool F16> __device__ inline bool not_finite8(i32x4 w) {
+  return not_finite2<F16>(w[0]) || not_finite2<F16>(w[1]) || not_finite2<F16>(w[2]) ||
+         not_finite2<F16>(w[3]);
+}
+// The e4m3 codes 0x7F and 0xFF are NaN; there are no infinities.
+__device__ inline bool nan_codes(i32x4 w) {
+  bool r = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int b = 0; b < 32; b += 8) r |= ((w[i] >> b) & 0x7F) == 0x7F;
+  return r;
+}
+
+// What a workgroup works on: a sequence, a key head and a split.
+struct Job {
+  int b, hk, split, tile0;
+  int t0, n;     // first row of q, drafted nodes
+  int ctx, len;  // cached positions before the nodes, positions in all
+  float sc;      // scale, key scale and log2 e: positive
+  bool flip, none;  // the sign of the scale goes to q; a zero scale: q is 0
+};
+
+// Workgroup -> job.  Workgroups go to the eight XCDs in turn; the row tiles
+// that share keys follow each other on one XCD and find them in its L2.  A
+// malformed plan gives wrong rows, never an access outside the buffers.
+__device__ inline bool find_job(const AttnArgs& a, Job& j) {
+  const int x = blockIdx.x >> 3;
+  int work = (x / a.ntiles) * 8 + (blockIdx.x & 7);
+  j.tile0 = x % a.ntiles;
+  if (work >= a.nwork) return false;
+  j.split = work % a.nsplit;
+  work /= a.nsplit;
+  j.hk = work % a.Hk;
+  j.b = work / a.Hk;
+  j.t0 = a.offsets[j.b];
+  const int64_t t1 = a.offsets[j.b + 1];
+  if (j.t0 < 0 || t1 <= j.t0 || t1 > a.T) return false;
+  j.n = (int)(t1 - j.t0);
+  j.ctx = max(a.context[j.b], 0);
+  j.len = (int)min((int64_t)j.ctx + j.n, (int64_t)a.max_pages << a.page_log);
+  const float sc = a.scale_log2e * (a.k_scale ? a.k_scale[j.hk] : 1.f);
+  j.flip = sc < 0.f;
+  j.none = sc == 0.f;
+  j.sc = j.none ? 1.f : fabsf(sc);
+  return true;
+}
+
+// Positions [lo, hi) of a split for the rows of a tile that ends with node
+// `last`, and how many splits those rows have.
+__device__ inline int split_range(const AttnArgs& a, const Job& j, int last, int& lo, int& hi) {
+  const int all = a.mask ? j.len : min(j.len, j.ctx + last + 1);
+  lo = j.split * a.chunk;
+  // the last split takes what the bound did not foresee
+  hi = j.split == a.nsplit - 1 ? all : min(all, lo + a.chunk);
+  return a.nsplit == 1 ? 1 : min(a.nsplit, (all + a.chunk - 1) / a.chunk);
+}
+
+// Which of the four positions pos .. pos + 3 the row of `node` (mask words
+// `mrow`) sees, as bits 0 .. 3; positions from hi on are not.
+__device__ inline uint32_t sees4(const AttnArgs& a, const Job& j, int node, const int64_t* mrow,
+                                 int pos, int hi) {
+  const int d = pos - j.ctx;  // in nodes; the context lies below 0
+  const uint32_t in = (1u << min(max(hi - pos, 0), 4)) - 1;
+  if (!a.mask) return in & ((1u << min(max(node + 1 - d, 0), 4)) - 1);
+  // the two words that hold the bits: all ones in the context, none past the last
+  const int w = d >> 6, sh = d & 63, top = a.mask_words - 1;
+  uint64_t w0 = top >= 0 ? (uint64_t)mrow[min(max(w, 0), top)] : 0;
+  uint64_t w1 = top >= 0 ? (uint64_t)mrow[min(max(w + 1, 0), top)] : 0;
+  w0 = w < 0 ? ~0ull : w > top ? 0 : w0;
+  w1 = w + 1 < 0 ? ~0ull : w + 1 > top ? 0 : w1;
+  return in & (uint32_t)((w0 >> sh) | (w1 << 1 << (63 - sh)));
+}
+
+// The signs of eight 16-bit floats, or all of them zero.
+__device__ inline i32x4 scaled_q(i32x4 q, bool flip, bool zero) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q[i] = zero ? 0 : flip ? q[i] ^ (int)0x80008000 : q[i];
+  return q;
+}
+
+// The running maximum moves only when it grows by more than 2^8 for some row
+// of the wave: until then the weights stay below 2^8 of the kept one, which
+// costs no precision, and the sums need no rescaling.
+constexpr float SLACK = 8.f;
+
+// O / l, rounded, and the row's lse from m (base 2) and l.
+__device__ inline float inverse_sum(float l, float vscale) {
+  return l > 0.f || l != l ? vscale / l : 0.f;
+}
+__device__ inline float row_lse(float m, float l) {
+  return (m + __builtin_amdgcn_logf(l)) * 0.69314718056f;
+}
+
+// ------------------------------------------------------------ few rows
+// NQ tiles of 16 rows.  S^T tiles are 16x16 (MFMA 16x16x32): lane l holds row
+// l % 16 and positions 4 (l / 16) + 0..3 of each, so two tiles of a block of
+// 32 positions make the eight positions of one lane in the second product;
+// the transposing reads of V take the same eight.
+template <int D, bool KV8> constexpr int stream_tile_bytes() { return 32 * D * (KV8 ? 1 : 2); }
+template <int D, int NQ, bool KV8> constexpr int stream_lds_bytes() {
+  // the waves' values; at the end two waves' sums, and all waves' m and l
+  return std::max(4 * stream_tile_bytes<D, KV8>(), 2 * NQ * 16 * D * 4) + 4 * NQ * 16 * 8;
+}
+
+template <int D, int NQ, bool F16, bool KV8>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs a) {
+  constexpr int ES = KV8 ? 1 : 2;
+  constexpr int RB = D * ES;           // bytes of a cache row
+  constexpr int KS = D / 32;           // steps of the first product
+  constexpr int DT = D / 16;           // tiles of the second
+  constexpr int NK = RB / 64;          // 16-byte loads of a key row per lane
+  constexpr int RPI = 1024 / RB;       // value rows of one load instruction
+  constexpr int NV = 32 / RPI;         // load instructions of a block's values
+  constexpr int CPR = RB / 16;         // chunks of a row
+  constexpr int VT = stream_tile_bytes<D, KV8>();
+
+  extern __shared__ __align__(16) char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int grp = lane >> 4, col = lane & 15;
+  char* const sv = smem + wave * VT;
+  float* const st = (float*)(smem + stream_lds_bytes<D, NQ, KV8>() - 4 * NQ * 16 * 8);
+
+  Job j;
+  if (!find_job(a, j)) return;
+  const int* const table = a.table + (int64_t)j.b * a.table_stride;
+  const char* const kb = (const char*)a.k + j.hk * a.k_hs * ES;
+  const char* const vb = (const char*)a.v + j.hk * a.v_hs * ES;
+  const int64_t k_ps = a.k_ps * ES, k_ts = a.k_ts * ES, v_ps = a.v_ps * ES, v_ts = a.v_ts * ES;
+  const int nrows = j.n * a.G;
+
+  for (int tile = j.tile0; tile * (16 * NQ) < nrows; tile += a.ntiles) {
+    const int row0 = tile * 16 * NQ;
+    const int last = min(row0 + 16 * NQ - 1, nrows - 1) / a.G;
+    int lo, hi;
+    const int nsp = split_range(a, j, last, lo, hi);
+    if (j.split >= nsp) continue;
+    const int nblk = (hi - lo + 31) / 32;
+
+    // this lane's rows, as operands of the first product
+    bool live[NQ];
+    int node[NQ];
+    i32x4 qf[NQ][KS];
+    const int64_t* mrow[NQ];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      const int row = row0 + q * 16 + col;
+      live[q] = row < nrows;
+      node[q] = live[q] ? row / a.G : 0;
+      const int64_t t = j.t0 + node[q];
+      const int head = j.hk * a.G + (live[q] ? row % a.G : 0);
+      const uint16_t* qp = a.q + t * a.q_ts + head * a.q_hs;
+      mrow[q] = a.mask ? a.mask + t * a.mask_words : nullptr;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        // a lane's 16 bytes of codes are two steps' operands
+        const int d = KV8 ? (ks >> 1) * 64 + grp * 16 + (ks & 1) * 8 : ks * 32 + grp * 8;
+        qf[q][ks] = scaled_q(*(const i32x4*)(qp + d), j.flip, j.none || !live[q]);
+      }
+    }
+
+    float m[NQ], l[NQ];
+    f32x4 o[NQ][DT];
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      m[q] = NEG_INF;
+      l[q] = 0.f;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) o[q][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // Pages of a block's 32 positions, one per lane (twice).
+    auto load_pages = [&](int blk) {
+      const int pos = min(lo + blk * 32 + (lane & 31), hi - 1);
+      return min(max(table[pos >> a.page_log], 0), a.pages - 1);
+    };
+    i32x4 kr[2][NK], vr[NV];
+    auto load_block = [&](int blk, int pg) {
+      const int base = lo + blk * 32;
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        const int r = min(base + kt * 16 + col, hi - 1) - base;
+        const int p = __shfl(pg, r);
+        const char* at = kb + p * k_ps + ((base + r) & a.page_mask) * k_ts + grp * 16;
+#pragma unroll
+        for (int i = 0; i < NK; ++i) kr[kt][i] = *(const i32x4*)(at + i * 64);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int r = min(base + i * RPI + lane / CPR, hi - 1) - base;
+        const int p = __shfl(pg, r);
+        vr[i] = *(const i32x4*)(vb + p * v_ps + ((base + r) & a.page_mask) * v_ts +
+                                (lane % CPR) * 16);
+      }
+    };
+    // Chunks of a value row are XOR-ed with the row, so that the transposing
+    // reads of 16 rows spread over the banks.
+    auto v_at = [&](int row, int chunk) {
+      return sv + row * RB + ((chunk ^ ((KV8 ? row : 2 * row) & (CPR - 1))) << 4);
+    };
+
+    int blk = wave;
+    int pg = 0;
+    if (blk < nblk) {
+      load_block(blk, load_pages(blk));
+      if (blk + 4 < nblk) pg = load_pages(blk + 4);
+    }
+    for (; blk < nblk; blk += 4) {
+      const int base = lo + blk * 32;
+      const bool tail = base + 32 > min(j.ctx, hi);
+      bool odd = false;
+      // Values past the end read as zero.  Drafted values that some rows do
+      // not see must not reach them: an infinity or NaN among those takes
+      // the slow product below.
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int r = i * RPI + lane / CPR;
+        if (tail) {
+          if (base + r >= hi) vr[i] = i32x4{0, 0, 0, 0};
+          else if (base + r >= j.ctx) odd |= KV8 ? nan_codes(vr[i]) : not_finite8<F16>(vr[i]);
+        }
+        *(i32x4*)v_at(r, lane % CPR) = vr[i];
+      }
+      odd = __any(odd);
+      f32x4 s[NQ][2];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) s[q][kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          i32x4 kf;
+          if constexpr (KV8)
+            kf = widen8<F16>(kr[kt][ks >> 1][2 * (ks & 1)], kr[kt][ks >> 1][2 * (ks & 1) + 1]);
+          else
+            kf = kr[kt][ks];
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) s[q][kt] = mfma16<F16>(kf, qf[q][ks], s[q][kt]);
+        }
+      }
+      if (blk + 4 < nblk) {
+        load_block(blk + 4, pg);
+        if (blk + 8 < nblk) pg = load_pages(blk + 8);
+      }
+      i32x4 pf[NQ];
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        if (tail) {
+#pragma unroll
+          for (int kt = 0; kt < 2; ++kt) {
+            const uint32_t vis = sees4(a, j, node[q], mrow[q], base + kt * 16 + grp * 4, hi);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[q][kt][i] = (vis >> i) & 1 ? s[q][kt][i] : NEG_INF;
+          }
+        }
+        float mx = s[q][0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[q][i >> 2][i & 3]);
+        const float mn = fmaxf(m[q], quad_max(mx));
+        if (__any((mn - m[q]) * j.sc > SLACK)) {
+          const float f = mn == NEG_INF ? 1.f : exp2_fast((m[q] - mn) * j.sc);
+          m[q] = mn;
+          l[q] *= f;
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[q][dt][i] *= f;
+        }
+        const float ms = m[q] == NEG_INF ? 0.f : m[q] * j.sc;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          s[q][i >> 2][i & 3] = exp2_fast(fmaf(s[q][i >> 2][i & 3], j.sc, -ms));
+          sum += s[q][i >> 2][i & 3];
+        }
+        l[q] += sum;
+        // rounded to the value type: the products are then exact in the MFMA
+        // and summed in 32 bits
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+          pf[q][w] = pack2<F16>(s[q][w >> 1][2 * (w & 1)], s[q][w >> 1][2 * (w & 1) + 1]);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();  // the lanes' values are in LDS
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+      if (odd) {
+        // One position at a time: a weight of zero adds nothing, whatever
+        // the value there is.
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt)
+#pragma unroll 1
+            for (int r = 0; r < 32; ++r) {
+              float p = 0.f;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if ((r >> 4) * 4 + (r & 3) == i) p = s[q][i >> 2][i & 3];
+              p = __shfl(p, ((r >> 2) & 3) * 16 + col);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int d = dt * 16 + grp * 4 + i;
+                const char* at = v_at(r, d * ES / 16) + (d * ES) % 16;
+                float v;
+                if constexpr (KV8) v = __builtin_amdgcn_cvt_f32_fp8(*(const uint8_t*)at, 0);
+                else v = h_to_f32<F16>(*(const uint16_t*)at);
+                if (p != 0.f) o[q][dt][i] += p * v;
+              }
+            }
+      } else {
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+          i32x4 vf;
+          if constexpr (KV8) {
+            const int r8 = col >> 1;
+            const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(lds_char*)(
+                v_at((r8 & 3) + 4 * grp + (r8 >> 2) * 16, dt) + (col & 1) * 8));
+            vf = widen8<F16>(w[0], w[1]);
+          } else {
+            const int r = 4 * grp + (col >> 2), c = 2 * dt + ((col & 3) >> 1), b8 = (col & 1) * 8;
+            const i32x2 w0 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                           (lds_s16x4*)(lds_char*)(v_at(r, c) + b8)));
+            const i32x2 w1 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                           (lds_s16x4*)(lds_char*)(v_at(r + 16, c) + b8)));
+            vf = i32x4{w0[0], w0[1], w1[0], w1[1]};
+          }
+#pragma unroll
+          for (int q = 0; q < NQ; ++q) o[q][dt] = mfma16<F16>(vf, pf[q], o[q][dt]);
+        }
+      }
+      __builtin_amdgcn_wave_barrier();  // read before the next block's are written
+    }
+
+    // Join the four waves.
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      l[q] = quad_sum(l[q]);
+      m[q] *= j.sc;
+      if (grp == 0) {
+        st[((wave * NQ + q) * 16 + col) * 2] = m[q];
+        st[((wave * NQ + q) * 16 + col) * 2 + 1] = l[q];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < NQ; ++q) {
+      float M = NEG_INF, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, st[((w * NQ + q) * 16 + col) * 2]);
+      const float ms = M == NEG_INF ? 0.f : M;
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        L += st[((w * NQ + q) * 16 + col) * 2 + 1] *
+             exp2_fast(st[((w * NQ + q) * 16 + col) * 2] - ms);
+      const float f = exp2_fast(m[q] - ms);
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[q][dt][i] *= f;
+      m[q] = M;
+      l[q] = L;
+    }
+    f32x4* const sums = (f32x4*)smem;
+#pragma unroll
+    for (int step = 2; step > 0; step >>= 1) {
+      if (wave >= step && wave < 2 * step) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt)
+            sums[((wave - step) * NQ * DT + q * DT + dt) * 64 + lane] = o[q][dt];
+      }
+      __syncthreads();
+      if (wave < step) {
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) o[q][dt] += sums[(wave * NQ * DT + q * DT + dt) * 64 + lane];
+      }
+      __syncthreads();
+    }
+    if (wave == 0) {
+      const float vscale = a.v_scale ? a.v_scale[j.hk] : 1.f;
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) {
+        if (!live[q]) continue;
+        const int row = row0 + q * 16 + col;
+        const int64_t r = (int64_t)(j.t0 + node[q]) * (a.Hk * a.G) + j.hk * a.G + row % a.G;
+        if (nsp == 1) {
+          const float inv = inverse_sum(l[q], vscale);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt)
+            *(i32x2*)(a.out + r * D + dt * 16 + grp * 4) =
+                i32x2{pack2<F16>(o[q][dt][0] * inv, o[q][dt][1] * inv),
+                      pack2<F16>(o[q][dt][2] * inv, o[q][dt][3] * inv)};
+          if (a.lse && grp == 0) a.lse[r] = row_lse(m[q], l[q]);
+        } else {
+          const int64_t pr = (int64_t)j.split * a.rows + r;
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) *(f32x4*)(a.part_o + pr * D + dt * 16 + grp * 4) = o[q][dt];
+          if (grp == 0) *(float2*)(a.part_ml + pr * 2) = make_float2(m[q], l[q]);
+        }
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ many rows
+// A tile in LDS holds its rows as 16-byte chunks; the chunk index is XOR-ed
+// with the row so that 32 lanes that read one chunk of 32 rows (K) or four
+// rows of two chunks (V, transposing reads) use all banks.
 template <int D> __device__ inline int k_off(int row, int chunk) {
   return row * (D * 2) + ((chunk ^ (row & (D / 8 - 1))) << 4);
 }
@@ -93,84 +527,54 @@ template <int D> __device__ inline int v_off(int row, int chunk) {
   return row * (D * 2) + ((chunk ^ ((row << 1) & (D / 8 - 1))) << 4);
 }
 
-struct Seq {
-  int t0, n;     // first row of q, drafted nodes
-  int ctx, len;  // cached positions before the nodes, positions in all
-};
+// Positions of a tile.
+template <int D> constexpr int tile_positions() { return 8192 / D; }
 
-template <int D, int RW, bool F16, bool KV8>
-__global__ __launch_bounds__(AT_THREADS) void attn_kernel(AttnArgs a) {
-  constexpr int CW = 4 / RW;
-  constexpr int BM = 32 * RW;             // rows per workgroup
-  constexpr int BN = CW == 4 ? 128 : 64;  // positions per tile
-  constexpr int NS = BN / (32 * CW);      // 32-position blocks per wave and tile
+// NW waves of 32 rows.  S^T tiles are 32x32 (MFMA 32x32x16): lane l holds row
+// l % 32 and positions 8 b + 4 (l / 32) + 0..3 of each.
+template <int D, int NW, bool F16, bool KV8>
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void tile_kernel(AttnArgs a) {
+  constexpr int BM = 32 * NW, BN = tile_positions<D>(), TH = NW * 64;
+  constexpr int NS = BN / 32;
   constexpr int DT = D / 32, KS = D / 16;
-  constexpr int CPR = KV8 ? D / 16 : D / 8;  // 16-byte chunks of a cache row
-  constexpr int NI = BN * CPR / AT_THREADS;  // chunks per thread, tile and operand
-  constexpr int TILE = BN * D * 2;           // bytes of one operand's tile
+  constexpr int ES = KV8 ? 1 : 2;
+  constexpr int CPR = D * ES / 16;       // 16-byte chunks of a cache row
+  constexpr int NI = BN * CPR / TH;      // chunks per thread, tile and operand
+  constexpr int TILE = BN * D * 2;       // bytes of one operand's tile
+  static_assert(NI * TH == BN * CPR, "whole chunks per thread");
 
-  extern __shared__ __align__(16) char smem[];
-  char* const sk = smem;
-  char* const sv = smem + TILE;
-
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  extern __shared__ __align__(16) char smem[];  // [2][keys, values]
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = lane >> 5, col = lane & 31;
-  const int rw = wave / CW, cw = wave % CW;
 
-  // Workgroup -> (sequence, key head, split, row tile).  Workgroups go to
-  // the eight XCDs in turn; the row tiles that share keys follow each other
-  // on one XCD and find them in its L2.
-  const int id = blockIdx.x;
-  const int x = id >> 3;
-  int work = (x / a.ntiles) * 8 + (id & 7);
-  const int tile0 = x % a.ntiles;
-  if (work >= a.nwork) return;
-  const int split = work % a.nsplit;
-  work /= a.nsplit;
-  const int hk = work % a.Hk, b = work / a.Hk;
+  Job j;
+  if (!find_job(a, j)) return;
+  const int* const table = a.table + (int64_t)j.b * a.table_stride;
+  const char* const kb = (const char*)a.k + j.hk * a.k_hs * ES;
+  const char* const vb = (const char*)a.v + j.hk * a.v_hs * ES;
+  const int64_t k_ps = a.k_ps * ES, k_ts = a.k_ts * ES, v_ps = a.v_ps * ES, v_ts = a.v_ts * ES;
+  const int nrows = j.n * a.G;
 
-  Seq s;
-  s.t0 = a.offsets[b];
-  s.n = a.offsets[b + 1] - s.t0;
-  s.ctx = a.context[b];
-  // A malformed plan gives wrong rows, never an access outside the buffers.
-  if (s.t0 < 0 || s.n <= 0 || (int64_t)s.t0 + s.n > a.T) return;
-  s.ctx = max(s.ctx, 0);
-  const int64_t room = (int64_t)a.max_pages << a.page_log;
-  s.len = (int)min((int64_t)s.ctx + s.n, room);
-  if (s.len <= 0) return;
-  const int G = a.G;
-  const int* const table = a.table + (int64_t)b * a.table_stride;
-  const float kscale = a.k_scale ? a.k_scale[hk] : 1.f;
-  const float vscale = a.v_scale ? a.v_scale[hk] : 1.f;
-  const float sc = a.scale_log2e * kscale;
-
-  const int nrows = s.n * G;
-  for (int tile = tile0; tile * BM < nrows; tile += a.ntiles) {
+  for (int tile = j.tile0; tile * BM < nrows; tile += a.ntiles) {
     const int row0 = tile * BM;
-    const int last_node = min(row0 + BM - 1, nrows - 1) / G;
-    const int kv_all = a.mask ? s.len : min(s.len, s.ctx + last_node + 1);
-    const int nsp = a.nsplit == 1 ? 1 : min(a.nsplit, (kv_all + a.chunk - 1) / a.chunk);
-    if (split >= nsp) continue;
-    const int kv_lo = split * a.chunk;
-    // the last split takes what the bound did not foresee
-    const int kv_hi = split == a.nsplit - 1 ? kv_all : min(kv_all, kv_lo + a.chunk);
-    const int ntl = (kv_hi - kv_lo + BN - 1) / BN;
+    const int last = min(row0 + BM - 1, nrows - 1) / a.G;
+    int lo, hi;
+    const int nsp = split_range(a, j, last, lo, hi);
+    if (j.split >= nsp) continue;
+    const int ntl = (hi - lo + BN - 1) / BN;
 
-    // this lane's row
-    const int row = row0 + rw * 32 + col;
+    const int row = row0 + wave * 32 + col;
     const bool live = row < nrows;
-    const int node = live ? row / G : 0;
-    const int64_t t = s.t0 + node;
-    const int head = hk * G + (live ? row % G : 0);
+    const int node = live ? row / a.G : 0;
+    const int64_t t = j.t0 + node;
+    const int head = j.hk * a.G + (live ? row % a.G : 0);
     i32x4 qf[KS];
     {
       const uint16_t* qp = a.q + t * a.q_ts + head * a.q_hs + half * 8;
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        qf[ks] = *(const i32x4*)(qp + ks * 16);
-        if (!live) qf[ks] = i32x4{0, 0, 0, 0};
-      }
+      for (int ks = 0; ks < KS; ++ks)
+        qf[ks] = scaled_q(*(const i32x4*)(qp + ks * 16), j.flip, j.none || !live);
     }
     const int64_t* const mrow = a.mask ? a.mask + t * a.mask_words : nullptr;
 
@@ -181,323 +585,275 @@ __global__ __launch_bounds__(AT_THREADS) void attn_kernel(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
 
-    int pg[NI];         // pages of the rows this thread loads next
+    int pg[NI];  // pages of the rows this thread loads next
     i32x4 rk[NI], rv[NI];
     auto load_pages = [&](int it) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int pos = min(kv_lo + it * BN + (tid + i * AT_THREADS) / CPR, kv_hi - 1);
+        const int pos = min(lo + it * BN + (tid + i * TH) / CPR, hi - 1);
         pg[i] = min(max(table[pos >> a.page_log], 0), a.pages - 1);
       }
     };
     auto load_tile = [&](int it) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int idx = tid + i * AT_THREADS;
-        const int r = idx / CPR, c = idx % CPR;
-        const int pos = min(kv_lo + it * BN + r, kv_hi - 1);
-        const int in = pos & a.page_mask;
-        const int64_t ko = pg[i] * a.k_ps + hk * a.k_hs + in * a.k_ts;
-        const int64_t vo = pg[i] * a.v_ps + hk * a.v_hs + in * a.v_ts;
-        rk[i] = *(const i32x4*)((const char*)a.k + (KV8 ? ko : ko * 2) + c * 16);
-        rv[i] = *(const i32x4*)((const char*)a.v + (KV8 ? vo : vo * 2) + c * 16);
+        const int idx = tid + i * TH;
+        const int in = min(lo + it * BN + idx / CPR, hi - 1) & a.page_mask;
+        rk[i] = *(const i32x4*)(kb + pg[i] * k_ps + in * k_ts + (idx % CPR) * 16);
+        rv[i] = *(const i32x4*)(vb + pg[i] * v_ps + in * v_ts + (idx % CPR) * 16);
       }
     };
-    load_pages(0);
-    load_tile(0);
-    if (ntl > 1) load_pages(1);
-
-    for (int it = 0; it < ntl; ++it) {
-      const int base = kv_lo + it * BN;
-      // Positions past the end read as zero; drafted values that some rows
-      // do not see must not reach them, so an infinity or NaN among those
-      // takes the slow product below.
-      const bool tail = base + BN > min(s.ctx, kv_hi);
+    // Stores the loaded tile; says whether drafted values of it that some
+    // rows may not see hold an infinity or NaN (positions past the end are
+    // stored as zero).
+    auto store_tile = [&](int it) {
+      const int base = lo + it * BN;
+      const bool tail = base + BN > min(j.ctx, hi);
+      char* const sk = smem + (it & 1) * 2 * TILE;
+      char* const sv = sk + TILE;
       bool odd = false;
-      __syncthreads();  // the previous tile is read
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int idx = tid + i * AT_THREADS;
+        const int idx = tid + i * TH;
         const int r = idx / CPR, c = idx % CPR;
-        if (tail && base + r >= kv_hi) {
-          rk[i] = i32x4{0, 0, 0, 0};
-          rv[i] = i32x4{0, 0, 0, 0};
+        if (tail) {
+          if (base + r >= hi) rk[i] = rv[i] = i32x4{0, 0, 0, 0};
+          else if (base + r >= j.ctx) odd |= KV8 ? nan_codes(rv[i]) : not_finite8<F16>(rv[i]);
         }
         if constexpr (KV8) {
-          i32x4 lo, hi;
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            lo[2 * w] = widen2<F16, false>(rk[i][w]);
-            lo[2 * w + 1] = widen2<F16, true>(rk[i][w]);
-            hi[2 * w] = widen2<F16, false>(rk[i][w + 2]);
-            hi[2 * w + 1] = widen2<F16, true>(rk[i][w + 2]);
-          }
-          *(i32x4*)(sk + k_off<D>(r, 2 * c)) = lo;
-          *(i32x4*)(sk + k_off<D>(r, 2 * c + 1)) = hi;
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            lo[2 * w] = widen2<F16, false>(rv[i][w]);
-            lo[2 * w + 1] = widen2<F16, true>(rv[i][w]);
-            hi[2 * w] = widen2<F16, false>(rv[i][w + 2]);
-            hi[2 * w + 1] = widen2<F16, true>(rv[i][w + 2]);
-          }
-          *(i32x4*)(sv + v_off<D>(r, 2 * c)) = lo;
-          *(i32x4*)(sv + v_off<D>(r, 2 * c + 1)) = hi;
-          if (tail && base + r >= s.ctx)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) odd |= not_finite2<F16>(lo[w]) || not_finite2<F16>(hi[w]);
+          *(i32x4*)(sk + k_off<D>(r, 2 * c)) = widen8<F16>(rk[i][0], rk[i][1]);
+          *(i32x4*)(sk + k_off<D>(r, 2 * c + 1)) = widen8<F16>(rk[i][2], rk[i][3]);
+          *(i32x4*)(sv + v_off<D>(r, 2 * c)) = widen8<F16>(rv[i][0], rv[i][1]);
+          *(i32x4*)(sv + v_off<D>(r, 2 * c + 1)) = widen8<F16>(rv[i][2], rv[i][3]);
         } else {
           *(i32x4*)(sk + k_off<D>(r, c)) = rk[i];
           *(i32x4*)(sv + v_off<D>(r, c)) = rv[i];
-          if (tail && base + r >= s.ctx)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) odd |= not_finite2<F16>(rv[i][w]);
         }
       }
-      if (tail) odd = __syncthreads_or(odd);
-      else __syncthreads();
+      if (tail) return __syncthreads_or(odd) != 0;
+      __syncthreads();
+      return false;
+    };
+
+    load_pages(0);
+    load_tile(0);
+    if (ntl > 1) load_pages(1);
+    bool odd = store_tile(0);
+    for (int it = 0; it < ntl; ++it) {
+      const int base = lo + it * BN;
+      const bool tail = base + BN > min(j.ctx, hi);
+      const char* const sk = smem + (it & 1) * 2 * TILE;
+      const char* const sv = sk + TILE;
       if (it + 1 < ntl) {
         load_tile(it + 1);
         if (it + 2 < ntl) load_pages(it + 2);
       }
-
+      f32x16 p[NS];
 #pragma unroll
       for (int ns = 0; ns < NS; ++ns) {
-        const int sub = (cw * NS + ns) * 32;  // first row of this block in the tile
-        f32x16 p;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = 0.f;
+        for (int i = 0; i < 16; ++i) p[ns][i] = 0.f;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          const i32x4 kf = *(const i32x4*)(sk + k_off<D>(sub + col, 2 * ks + half));
-          p = mfma32<F16>(kf, qf[ks], p);
-        }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] *= sc;
-        if (tail) {
-#pragma unroll
-          for (int bb = 0; bb < 4; ++bb) {
-            const int pos0 = base + sub + 8 * bb + 4 * half;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int pos = pos0 + i, j = pos - s.ctx;
-              bool sees = pos < kv_hi;
-              if (sees && j >= 0) {
-                if (mrow)
-                  sees = (j >> 6) < a.mask_words && ((mrow[j >> 6] >> (j & 63)) & 1);
-                else
-                  sees = j <= node;
-              }
-              if (!sees) p[bb * 4 + i] = NEG_INF;
-            }
-          }
-        }
-        float mx = p[0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, p[i]);
-        const float mn = fmaxf(m, half_max(mx));
-        const float ms = mn == NEG_INF ? 0.f : mn;  // nothing seen yet: all weights are 0
-        const float f = exp2_fast(m - ms);
-        m = mn;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          p[i] = exp2_fast(p[i] - ms);
-          sum += p[i];
-        }
-        l = l * f + sum;
-        if (__any(f != 1.f)) {
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[dt][i] *= f;
-        }
-        if (odd) {
-          // One position at a time: a weight of zero adds nothing, whatever
-          // the value there is.
-          for (int j = 0; j < 32; ++j) {
-            float pj = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if ((j >> 3) * 4 + (j & 3) == i) pj = p[i];
-            pj = __shfl(pj, col + ((j >> 2) & 1) * 32);
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int d = dt * 32 + (i >> 2) * 8 + half * 4 + (i & 3);
-                const float v = h_to_f32<F16>(
-                    *(const uint16_t*)(sv + v_off<D>(sub + j, d >> 3) + (d & 7) * 2));
-                if (pj != 0.f) o[dt][i] += pj * v;
-              }
-          }
-        } else {
-          // The probabilities of 16 positions, rounded to the value type: the
-          // products are exact in the MFMA and summed in 32 bits.
-          i32x4 pf[2];
-#pragma unroll
-          for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-              pf[tt][w] = pack2<F16>(p[8 * tt + 2 * w], p[8 * tt + 2 * w + 1]);
-          const int i16 = lane & 15;
-          const int vr = sub + 4 * half + (i16 >> 2);
-          const int vc = 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
-#pragma unroll
-          for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt) {
-              s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (lds_s16x4*)(lds_char*)(sv + v_off<D>(vr + 16 * tt, vc + 4 * dt) + (i16 & 1) * 8));
-              s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                  (lds_s16x4*)(lds_char*)(sv + v_off<D>(vr + 16 * tt + 8, vc + 4 * dt) + (i16 & 1) * 8));
-              const i32x2 w0 = __builtin_bit_cast(i32x2, v0), w1 = __builtin_bit_cast(i32x2, v1);
-              o[dt] = mfma32<F16>(i32x4{w0[0], w0[1], w1[0], w1[1]}, pf[tt], o[dt]);
-            }
+          const i32x4 kf = *(const i32x4*)(sk + k_off<D>(ns * 32 + col, 2 * ks + half));
+          p[ns] = mfma32<F16>(kf, qf[ks], p[ns]);
         }
       }
+      if (tail) {
+#pragma unroll
+        for (int ns = 0; ns < NS; ++ns)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const uint32_t vis = sees4(a, j, node, mrow, base + ns * 32 + 8 * b + 4 * half, hi);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[ns][b * 4 + i] = (vis >> i) & 1 ? p[ns][b * 4 + i] : NEG_INF;
+          }
+      }
+      float mx = p[0][0];
+#pragma unroll
+      for (int i = 1; i < NS * 16; ++i) mx = fmaxf(mx, p[i >> 4][i & 15]);
+      const float mn = fmaxf(m, half_max(mx));
+      if (__any((mn - m) * j.sc > SLACK)) {
+        const float f = mn == NEG_INF ? 1.f : exp2_fast((m - mn) * j.sc);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[dt][i] *= f;
+      }
+      const float ms = m == NEG_INF ? 0.f : m * j.sc;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < NS * 16; ++i) {
+        p[i >> 4][i & 15] = exp2_fast(fmaf(p[i >> 4][i & 15], j.sc, -ms));
+        sum += p[i >> 4][i & 15];
+      }
+      l += sum;
+      if (odd) {
+        // One position at a time: a weight of zero adds nothing, whatever
+        // the value there is.
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll 1
+          for (int r = 0; r < BN; ++r) {
+            float w = 0.f;
+#pragma unroll
+            for (int i = 0; i < NS * 16; ++i)
+              if ((r >> 5) * 16 + ((r & 31) >> 3) * 4 + (r & 3) == i) w = p[i >> 4][i & 15];
+            w = __shfl(w, col + ((r >> 2) & 1) * 32);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int d = dt * 32 + (i >> 2) * 8 + half * 4 + (i & 3);
+              const float v =
+                  h_to_f32<F16>(*(const uint16_t*)(sv + v_off<D>(r, d >> 3) + (d & 7) * 2));
+              if (w != 0.f) o[dt][i] += w * v;
+            }
+          }
+      } else {
+        const int i16 = lane & 15;
+        const int vr = 4 * half + (i16 >> 2);
+        const int vc = 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
+#pragma unroll
+        for (int tt = 0; tt < 2 * NS; ++tt) {
+          i32x4 pf;  // sixteen positions' probabilities, rounded to the value type
+#pragma unroll
+          for (int w = 0; w < 4; ++w)
+            pf[w] = pack2<F16>(p[tt >> 1][8 * (tt & 1) + 2 * w], p[tt >> 1][8 * (tt & 1) + 2 * w + 1]);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) {
+            const i32x2 w0 = __builtin_bit_cast(
+                i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)(
+                           sv + v_off<D>(vr + 16 * tt, vc + 4 * dt) + (i16 & 1) * 8)));
+            const i32x2 w1 = __builtin_bit_cast(
+                i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)(
+                           sv + v_off<D>(vr + 16 * tt + 8, vc + 4 * dt) + (i16 & 1) * 8)));
+            o[dt] = mfma32<F16>(i32x4{w0[0], w0[1], w1[0], w1[1]}, pf, o[dt]);
+          }
+        }
+      }
+      // The other buffer was last read before the previous barrier.
+      if (it + 1 < ntl) odd = store_tile(it + 1);
     }
 
-    // Join the waves that share rows.
     l = half_sum(l);
-    if constexpr (CW > 1) {
-      __syncthreads();  // the tiles are read
-      float* const st = (float*)smem;  // [4][32][2]
-      if (half == 0) {
-        st[(wave * 32 + col) * 2] = m;
-        st[(wave * 32 + col) * 2 + 1] = l;
-      }
-      __syncthreads();
-      float M = NEG_INF, L = 0.f;
-#pragma unroll
-      for (int c = 0; c < CW; ++c) M = fmaxf(M, st[((rw * CW + c) * 32 + col) * 2]);
-      const float ms = M == NEG_INF ? 0.f : M;
-#pragma unroll
-      for (int c = 0; c < CW; ++c)
-        L += st[((rw * CW + c) * 32 + col) * 2 + 1] *
-             exp2_fast(st[((rw * CW + c) * 32 + col) * 2] - ms);
-      const float f = exp2_fast(m - ms);
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[dt][i] *= f;
-      m = M;
-      l = L;
-      // pairwise: the upper half of the waves hands its sums to the lower
-#pragma unroll
-      for (int step = CW / 2; step > 0; step >>= 1) {
-        __syncthreads();
-        if (cw >= step && cw < 2 * step) {
-          float* const dst = (float*)smem + (rw * step + (cw - step)) * (DT * 16 * 64) + lane;
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) dst[(dt * 16 + i) * 64] = o[dt][i];
-        }
-        __syncthreads();
-        if (cw < step) {
-          const float* const src = (const float*)smem + (rw * step + cw) * (DT * 16 * 64) + lane;
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[dt][i] += src[(dt * 16 + i) * 64];
-        }
-      }
-    }
-    if (cw == 0 && live) {
-      const int64_t r = t * ((int64_t)a.Hk * G) + head;
-      if (a.nsplit > 1 && half == 0 && split == 0) a.nsp[r] = nsp;
+    m *= j.sc;
+    if (live) {
+      const int64_t r = t * ((int64_t)a.Hk * a.G) + head;
       if (nsp == 1) {
-        const float inv = l > 0.f || l != l ? vscale / l : 0.f;
-        uint16_t* const op = a.out + r * D;
+        const float inv = inverse_sum(l, a.v_scale ? a.v_scale[j.hk] : 1.f);
+        uint16_t* const op = a.out + r * D + half * 4;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-          for (int bb = 0; bb < 4; ++bb) {
-            i32x2 w;
-            w[0] = pack2<F16>(o[dt][bb * 4] * inv, o[dt][bb * 4 + 1] * inv);
-            w[1] = pack2<F16>(o[dt][bb * 4 + 2] * inv, o[dt][bb * 4 + 3] * inv);
-            *(i32x2*)(op + dt * 32 + bb * 8 + half * 4) = w;
-          }
-        if (a.lse && half == 0) a.lse[r] = (m + __log2f(l)) * 0.69314718056f;
+          for (int b = 0; b < 4; ++b)
+            *(i32x2*)(op + dt * 32 + b * 8) =
+                i32x2{pack2<F16>(o[dt][b * 4] * inv, o[dt][b * 4 + 1] * inv),
+                      pack2<F16>(o[dt][b * 4 + 2] * inv, o[dt][b * 4 + 3] * inv)};
+        if (a.lse && half == 0) a.lse[r] = row_lse(m, l);
       } else {
-        const int64_t pr = (int64_t)split * a.rows + r;
-        float* const op = a.part_o + pr * D;
+        const int64_t pr = (int64_t)j.split * a.rows + r;
+        float* const op = a.part_o + pr * D + half * 4;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-          for (int bb = 0; bb < 4; ++bb)
-            *(f32x4*)(op + dt * 32 + bb * 8 + half * 4) =
-                f32x4{o[dt][bb * 4], o[dt][bb * 4 + 1], o[dt][bb * 4 + 2], o[dt][bb * 4 + 3]};
-        if (half == 0) {
-          a.part_ml[pr * 2] = m;
-          a.part_ml[pr * 2 + 1] = l;
-        }
+          for (int b = 0; b < 4; ++b)
+            *(f32x4*)(op + dt * 32 + b * 8) =
+                f32x4{o[dt][b * 4], o[dt][b * 4 + 1], o[dt][b * 4 + 2], o[dt][b * 4 + 3]};
+        if (half == 0) *(float2*)(a.part_ml + pr * 2) = make_float2(m, l);
       }
     }
     __syncthreads();  // smem is written again for the next row tile
   }
 }
 
-// Joins the splits of each row: one wave per row, D / 64 values per lane.
+// ---------------------------------------------------------------- joining
+// Joins the splits: D / 4 lanes per row, blockIdx.y the group of rows.
 template <int D, bool F16>
-__global__ __launch_bounds__(AT_THREADS) void attn_join_kernel(AttnArgs a) {
-  const int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (r >= a.rows) return;
-  const int lane = threadIdx.x & 63;
-  // Rows that no sequence owns, and rows that one workgroup finished, are
-  // not touched: nsp was cleared before and set by the row's first split.
-  const int nsp = a.nsp[r];
-  if (nsp <= 1 || nsp > a.nsplit) return;
-  float M = NEG_INF;
-  for (int i = 0; i < nsp; ++i) M = fmaxf(M, a.part_ml[(i * a.rows + r) * 2]);
-  const float ms = M == NEG_INF ? 0.f : M;
-  float L = 0.f, o[D / 64];
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int bm) {
+  constexpr int LPR = D / 4, RPB = 256 / LPR;
+  const int hk = blockIdx.x % a.Hk, b = blockIdx.x / a.Hk;
+  Job j;
+  j.t0 = a.offsets[b];
+  const int64_t t1 = a.offsets[b + 1];
+  if (j.t0 < 0 || t1 <= j.t0 || t1 > a.T) return;
+  j.n = (int)(t1 - j.t0);
+  j.ctx = max(a.context[b], 0);
+  j.len = (int)min((int64_t)j.ctx + j.n, (int64_t)a.max_pages << a.page_log);
+  j.split = 0;
+  const int c = threadIdx.x % LPR;
+  for (int row = blockIdx.y * RPB + threadIdx.x / LPR; row < j.n * a.G; row += gridDim.y * RPB) {
+    int lo, hi;
+    const int last = min(row / bm * bm + bm - 1, j.n * a.G - 1) / a.G;
+    const int nsp = split_range(a, j, last, lo, hi);
+    if (nsp <= 1) continue;  // written by its workgroup
+    const int64_t r = (int64_t)(j.t0 + row / a.G) * (a.Hk * a.G) + hk * a.G + row % a.G;
+    float M = NEG_INF;
+    for (int i = 0; i < nsp; ++i) M = fmaxf(M, a.part_ml[(i * a.rows + r) * 2]);
+    const float ms = M == NEG_INF ? 0.f : M;
+    float L = 0.f;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < nsp; ++i) {
+      const int64_t pr = i * a.rows + r;
+      const float2 ml = *(const float2*)(a.part_ml + pr * 2);
+      const f32x4 p = *(const f32x4*)(a.part_o + pr * D + c * 4);
+      const float f = exp2_fast(ml.x - ms);
+      L += f * ml.y;
 #pragma unroll
-  for (int c = 0; c < D / 64; ++c) o[c] = 0.f;
-  for (int i = 0; i < nsp; ++i) {
-    const int64_t pr = i * a.rows + r;
-    const float f = exp2_fast(a.part_ml[pr * 2] - ms);
-    L += f * a.part_ml[pr * 2 + 1];
-#pragma unroll
-    for (int c = 0; c < D / 64; ++c) o[c] += f * a.part_o[pr * D + c * 64 + lane];
+      for (int e = 0; e < 4; ++e) o[e] += f * p[e];
+    }
+    const float inv = inverse_sum(L, a.v_scale ? a.v_scale[hk] : 1.f);
+    *(i32x2*)(a.out + r * D + c * 4) =
+        i32x2{pack2<F16>(o[0] * inv, o[1] * inv), pack2<F16>(o[2] * inv, o[3] * inv)};
+    if (a.lse && c == 0) a.lse[r] = row_lse(M, L);
   }
-  const int hk = (int)(r % (a.Hk * a.G)) / a.G;
-  const float vscale = a.v_scale ? a.v_scale[hk] : 1.f;
-  const float inv = L > 0.f || L != L ? vscale / L : 0.f;
-#pragma unroll
-  for (int c = 0; c < D / 64; ++c) a.out[r * D + c * 64 + lane] = f32_to_h<F16>(o[c] * inv);
-  if (a.lse && lane == 0) a.lse[r] = (M + __log2f(L)) * 0.69314718056f;
 }
 
-template <int D, int RW, bool F16, bool KV8>
+template <int D, int SHAPE, bool F16, bool KV8>
 hipError_t launch_one(const AttnArgs& a, hipStream_t s) {
-  constexpr int BN = RW == 1 ? 128 : 64;
-  constexpr size_t lds = (size_t)BN * D * 4;
-  const void* fn = (const void*)attn_kernel<D, RW, F16, KV8>;
-  hipError_t e = opt_in_lds(fn, lds);
-  if (e != hipSuccess) return e;
   const int64_t grid = (int64_t)((a.nwork + 7) / 8 * 8) * a.ntiles;
-  hipLaunchKernelGGL((attn_kernel<D, RW, F16, KV8>), dim3((unsigned)grid), dim3(AT_THREADS), lds,
-                     s, a);
+  hipError_t e;
+  if constexpr (SHAPE <= AT_STREAM32) {
+    constexpr int NQ = SHAPE == AT_STREAM16 ? 1 : 2;
+    constexpr size_t lds = stream_lds_bytes<D, NQ, KV8>();
+    e = opt_in_lds((const void*)stream_kernel<D, NQ, F16, KV8>, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((stream_kernel<D, NQ, F16, KV8>), dim3((unsigned)grid), dim3(256), lds, s, a);
+  } else {
+    constexpr int NW = SHAPE == AT_TILE128 ? 4 : 8;
+    constexpr size_t lds = tile_positions<D>() * D * 8;
+    e = opt_in_lds((const void*)tile_kernel<D, NW, F16, KV8>, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((tile_kernel<D, NW, F16, KV8>), dim3((unsigned)grid), dim3(NW * 64), lds, s,
+                       a);
+  }
   e = hipGetLastError();
   if (e != hipSuccess || a.nsplit == 1) return e;
-  hipLaunchKernelGGL((attn_join_kernel<D, F16>), dim3((unsigned)((a.rows + 3) / 4)),
-                     dim3(AT_THREADS), 0, s, a);
+  const int bm = attn_rows(SHAPE), rpb = 256 / (D / 4);
+  const int64_t groups = std::min<int64_t>(((int64_t)a.ntiles * bm + rpb - 1) / rpb, 65535);
+  hipLaunchKernelGGL((join_kernel<D, F16>),
+                     dim3((unsigned)(a.nwork / a.nsplit), (unsigned)groups), dim3(256), 0, s, a, bm);
   return hipGetLastError();
 }
 
-template <int D, int RW>
+template <int D, int SHAPE>
 hipError_t launch_types(const AttnArgs& a, bool f16, bool kv8, hipStream_t s) {
-  if (f16) return kv8 ? launch_one<D, RW, true, true>(a, s) : launch_one<D, RW, true, false>(a, s);
-  return kv8 ? launch_one<D, RW, false, true>(a, s) : launch_one<D, RW, false, false>(a, s);
+  if (f16) return kv8 ? launch_one<D, SHAPE, true, true>(a, s) : launch_one<D, SHAPE, true, false>(a, s);
+  return kv8 ? launch_one<D, SHAPE, false, true>(a, s) : launch_one<D, SHAPE, false, false>(a, s);
 }
 
 template <int D>
-hipError_t launch_dim(const AttnArgs& a, int rw, bool f16, bool kv8, hipStream_t s) {
-  if (rw == 1) return launch_types<D, 1>(a, f16, kv8, s);
-  if (rw == 2) return launch_types<D, 2>(a, f16, kv8, s);
-  return launch_types<D, 4>(a, f16, kv8, s);
+hipError_t launch_dim(const AttnArgs& a, int shape, bool f16, bool kv8, hipStream_t s) {
+  switch (shape) {
+    case AT_STREAM16: return launch_types<D, AT_STREAM16>(a, f16, kv8, s);
+    case AT_TILE128: return launch_types<D, AT_TILE128>(a, f16, kv8, s);
+  }
+  if constexpr (D < 256) {
+    if (shape == AT_STREAM32) return launch_types<D, AT_STREAM32>(a, f16, kv8, s);
+    if (shape == AT_TILE256) return launch_types<D, AT_TILE256>(a, f16, kv8, s);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -505,27 +861,40 @@ hipError_t launch_dim(const AttnArgs& a, int rw, bool f16, bool kv8, hipStream_t
 AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len) {
   AttnPlan p;
   const int64_t rows = max_nodes * G;
-  p.rw = rows <= 32 ? 1 : rows <= 64 ? 2 : 4;
-  const int bm = 32 * p.rw, bn = p.rw == 1 ? 128 : 64;
+  if (D == 256) p.shape = rows <= 16 ? AT_STREAM16 : AT_TILE128;  // what fits the registers
+  else p.shape = rows <= 16 ? AT_STREAM16 : rows <= 64 ? AT_STREAM32 : rows <= 128 ? AT_TILE128 : AT_TILE256;
+  const int bm = attn_rows(p.shape);
   p.ntiles = (rows + bm - 1) / bm;
-  // Enough workgroups for two on each of the 256 CUs; a split takes at
-  // least two tiles.
   const int64_t units = B * Hk * p.ntiles;
-  int64_t ns = (512 + units - 1) / units;
-  ns = std::max<int64_t>(1, std::min(ns, (max_len + 2 * bn - 1) / (2 * bn)));
-  p.chunk = ((max_len + ns - 1) / ns + bn - 1) / bn * bn;
+  const int64_t step = p.shape <= AT_STREAM32 ? 128 : 64;  // positions of one round of the waves
+  const int64_t steps = (max_len + step - 1) / step;
+  int64_t ns;
+  if (p.shape <= AT_STREAM32) {
+    // a few rounds of the 512 workgroups that run at a time, so that uneven
+    // lengths even out
+    ns = (1536 + units - 1) / units;
+    ns = std::min(ns, (steps + 1) / 2);
+  } else {
+    // as many as fill whole rounds best; splits of four tiles at least
+    const int64_t slots = p.shape == AT_TILE128 && D < 256 ? 512 : 256;
+    double best = 0;
+    ns = 1;
+    for (int64_t n = 1; n <= std::min<int64_t>(16, (steps + 3) / 4); ++n) {
+      const int64_t rounds = (units * n + slots - 1) / slots;
+      const double use = (double)(units * n) / (double)(rounds * slots) - 0.01 * (double)n;
+      if (use > best + 1e-9) { best = use; ns = n; }
+    }
+  }
+  ns = std::max<int64_t>(1, ns);
+  p.chunk = (steps + ns - 1) / ns * step;
   p.nsplit = std::max<int64_t>(1, (max_len + p.chunk - 1) / p.chunk);
   return p;
 }
 
-hipError_t launch_attention(const AttnArgs& a, int D, int rw, bool f16, bool kv8, hipStream_t s) {
-  if (a.nsplit > 1) {
-    hipError_t e = launch_fill_zero(a.nsp, (size_t)a.rows * sizeof(int), s);
-    if (e != hipSuccess) return e;
-  }
-  if (D == 64) return launch_dim<64>(a, rw, f16, kv8, s);
-  if (D == 128) return launch_dim<128>(a, rw, f16, kv8, s);
-  return launch_dim<256>(a, rw, f16, kv8, s);
+hipError_t launch_attention(const AttnArgs& a, int D, int shape, bool f16, bool kv8, hipStream_t s) {
+  if (D == 64) return launch_dim<64>(a, shape, f16, kv8, s);
+  if (D == 128) return launch_dim<128>(a, shape, f16, kv8, s);
+  return launch_dim<256>(a, shape, f16, kv8, s);
 }
 
 }  // namespace lg

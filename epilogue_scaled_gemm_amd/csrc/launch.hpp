@@ -178,22 +178,25 @@ struct AttnArgs {
   const float *k_scale, *v_scale;
   float* part_o;           // [nsplit][rows][D]
   float* part_ml;          // [nsplit][rows][2]
-  int* nsp;                // [rows]
   int64_t q_ts, q_hs, k_ps, k_hs, k_ts, v_ps, v_hs, v_ts;
   int64_t T, rows, table_stride;
   int Hk, G, mask_words, max_pages, pages, page_log, page_mask;
   int nwork, ntiles, nsplit, chunk;
   float scale_log2e;
 };
-// How a call is cut: rw row tiles of 32 per workgroup, ntiles workgroups over
-// a sequence's rows, nsplit splits of `chunk` positions.
+// How a call is cut: the kernel and its row tile, ntiles workgroups over a
+// sequence's rows, nsplit splits of `chunk` positions.
+enum AttnShape : int { AT_STREAM16 = 0, AT_STREAM32 = 1, AT_TILE128 = 2, AT_TILE256 = 3 };
+inline constexpr int attn_rows(int shape) {
+  return shape == AT_STREAM16 ? 16 : shape == AT_STREAM32 ? 32 : shape == AT_TILE128 ? 128 : 256;
+}
 struct AttnPlan {
-  int rw;
+  int shape;
   int64_t ntiles, nsplit, chunk;
 };
 AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len);
 // D is 64, 128 or 256.
-hipError_t launch_attention(const AttnArgs& a, int D, int rw, bool f16, bool kv8, hipStream_t s);
+hipError_t launch_attention(const AttnArgs& a, int D, int shape, bool f16, bool kv8, hipStream_t s);
 
 struct ScoreArgs {
   const void* logits;
