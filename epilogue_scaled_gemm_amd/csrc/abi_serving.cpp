@@ -189,6 +189,13 @@ int run_attention(lin_gemm_t h, const lin_attention_t* p, hipStream_t s) {
     return fail(h, LIN_ERR_INVALID_ARG, "the page table needs 1 .. 2^30 / page_size pages a row");
   if (p->mask_words > ((int64_t)1 << 20))
     return fail(h, LIN_ERR_UNSUPPORTED, "more than 2^20 mask words");
+  // The kernels step within a page with 32-bit byte offsets.
+  for (int64_t x : {p->k_page_stride, p->v_page_stride})
+    if (x < 0 || x >= ((int64_t)1 << 30))
+      return fail(h, LIN_ERR_UNSUPPORTED, "page strides must be in [0, 2^30)");
+  for (int64_t x : {p->k_in_page_stride, p->v_in_page_stride})
+    if (x < 0 || x >= ((int64_t)1 << 30) / p->page_size)
+      return fail(h, LIN_ERR_UNSUPPORTED, "a page must span less than 2^30 values");
   if (misaligned(p->q) || misaligned(p->out) ||
       any_not_multiple(8, {p->q_token_stride, p->q_head_stride}))
     return fail(h, LIN_ERR_UNSUPPORTED, "q, out and strides must be multiples of 16 bytes");

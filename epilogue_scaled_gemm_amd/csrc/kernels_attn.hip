@@ -28,6 +28,8 @@
 //    positions in LDS, double-buffered.
 // Long contexts are split over workgroups; those write (m, l, O) in 32 bits
 // and join_kernel joins them.
+#include <type_traits>
+
 #include "launch.hpp"
 
 namespace lg {
@@ -63,9 +65,16 @@ template <bool F16> __device__ inline f32x16 mfma32(i32x4 a, i32x4 b, f32x16 c) 
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Two fp32 -> packed 16-bit floats.
+// Two fp32 -> packed 16-bit floats (round to nearest even).
 template <bool F16> __device__ inline int pack2(float a, float b) {
-  return (int)((uint32_t)f32_to_h<F16>(a) | ((uint32_t)f32_to_h<F16>(b) << 16));
+  typedef __attribute__((ext_vector_type(2))) float f32x2;
+  if constexpr (F16) {
+    typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
+    return __builtin_bit_cast(int, __builtin_convertvector((f32x2{a, b}), f16x2));
+  } else {
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+    return __builtin_bit_cast(int, __builtin_convertvector((f32x2{a, b}), bf16x2));
+  }
 }
 
 // Two e4m3 codes (bytes 2 HI and 2 HI + 1 of w) -> packed 16-bit floats, exact.
@@ -120,6 +129,34 @@ __device__ inline bool nan_codes(i32x4 w) {
 #pragma unroll
     for (int b = 0; b < 32; b += 8) r |= ((w[i] >> b) & 0x7F) == 0x7F;
   return r;
+}
+
+// The slow product for tiles that hold infinities or NaN among drafted values:
+// a weight of zero must add nothing, whatever the value.  The values are
+// split into finite ones (others 0) and, one kind after the other, ones where
+// a value is +inf, -inf or NaN; a row's weight on such places makes its sum
+// that value.
+template <bool F16> __device__ inline i32x4 finite_part(i32x4 w) {
+  constexpr int E = F16 ? 0x7C00 : 0x7F80;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & E) == E) w[i] &= (int)0xFFFF0000;
+    if (((w[i] >> 16) & E) == E) w[i] &= 0xFFFF;
+  }
+  return w;
+}
+template <bool F16> __device__ inline i32x4 where_kind(i32x4 w, int kind) {
+  constexpr int E = F16 ? 0x7C00 : 0x7F80, ONE = F16 ? 0x3C00 : 0x3F80;
+  auto is = [&](int v) {  // 0: +inf, 1: -inf, 2: NaN
+    v &= 0xFFFF;
+    return kind == 0 ? v == E : kind == 1 ? v == (E | 0x8000) : (v & 0x7FFF) > E;
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (is(w[i]) ? ONE : 0) | (is(w[i] >> 16) ? ONE << 16 : 0);
+  return w;
+}
+__device__ inline float kind_value(int kind) {
+  return kind == 0 ? -NEG_INF : kind == 1 ? NEG_INF : __builtin_nanf("");
 }
 
 // What a workgroup works on: a sequence, a key head and a split.
@@ -237,7 +274,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
   const int* const table = a.table + (int64_t)j.b * a.table_stride;
   const char* const kb = (const char*)a.k + j.hk * a.k_hs * ES;
   const char* const vb = (const char*)a.v + j.hk * a.v_hs * ES;
-  const int64_t k_ps = a.k_ps * ES, k_ts = a.k_ts * ES, v_ps = a.v_ps * ES, v_ts = a.v_ts * ES;
+  // a page's bytes fit 32 bits (checked on the host), a cache's need not
+  const uint32_t k_ps = a.k_ps * ES, k_ts = a.k_ts * ES, v_ps = a.v_ps * ES, v_ts = a.v_ts * ES;
   const int nrows = j.n * a.G;
 
   for (int tile = j.tile0; tile * (16 * NQ) < nrows; tile += a.ntiles) {
@@ -283,16 +321,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
     // Pages of a block's 32 positions, one per lane (twice).
     auto load_pages = [&](int blk) {
       const int pos = min(lo + blk * 32 + (lane & 31), hi - 1);
-      return min(max(table[pos >> a.page_log], 0), a.pages - 1);
+      return table[pos >> a.page_log];  // not looked at before it is used: no wait here
     };
     i32x4 kr[2][NK], vr[NV];
     auto load_block = [&](int blk, int pg) {
       const int base = lo + blk * 32;
+      pg = min(max(pg, 0), a.pages - 1);
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
         const int r = min(base + kt * 16 + col, hi - 1) - base;
         const int p = __shfl(pg, r);
-        const char* at = kb + p * k_ps + ((base + r) & a.page_mask) * k_ts + grp * 16;
+        const char* at = kb + (uint64_t)(uint32_t)p * k_ps +
+                         (((base + r) & a.page_mask) * k_ts + grp * 16);
 #pragma unroll
         for (int i = 0; i < NK; ++i) kr[kt][i] = *(const i32x4*)(at + i * 64);
       }
@@ -300,8 +340,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
       for (int i = 0; i < NV; ++i) {
         const int r = min(base + i * RPI + lane / CPR, hi - 1) - base;
         const int p = __shfl(pg, r);
-        vr[i] = *(const i32x4*)(vb + p * v_ps + ((base + r) & a.page_mask) * v_ts +
-                                (lane % CPR) * 16);
+        vr[i] = *(const i32x4*)(vb + (uint64_t)(uint32_t)p * v_ps +
+                                (((base + r) & a.page_mask) * v_ts + (lane % CPR) * 16));
       }
     };
     // Chunks of a value row are XOR-ed with the row, so that the transposing
@@ -394,50 +434,38 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();  // the lanes' values are in LDS
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      if (odd) {
-        // One position at a time: a weight of zero adds nothing, whatever
-        // the value there is.
-#pragma unroll
-        for (int q = 0; q < NQ; ++q)
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-#pragma unroll 1
-            for (int r = 0; r < 32; ++r) {
-              float p = 0.f;
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if ((r >> 4) * 4 + (r & 3) == i) p = s[q][i >> 2][i & 3];
-              p = __shfl(p, ((r >> 2) & 3) * 16 + col);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int d = dt * 16 + grp * 4 + i;
-                const char* at = v_at(r, d * ES / 16) + (d * ES) % 16;
-                float v;
-                if constexpr (KV8) v = __builtin_amdgcn_cvt_f32_fp8(*(const uint8_t*)at, 0);
-                else v = h_to_f32<F16>(*(const uint16_t*)at);
-                if (p != 0.f) o[q][dt][i] += p * v;
-              }
-            }
-      } else {
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          i32x4 vf;
-          if constexpr (KV8) {
-            const int r8 = col >> 1;
-            const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(lds_char*)(
-                v_at((r8 & 3) + 4 * grp + (r8 >> 2) * 16, dt) + (col & 1) * 8));
-            vf = widen8<F16>(w[0], w[1]);
-          } else {
-            const int r = 4 * grp + (col >> 2), c = 2 * dt + ((col & 3) >> 1), b8 = (col & 1) * 8;
-            const i32x2 w0 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                           (lds_s16x4*)(lds_char*)(v_at(r, c) + b8)));
-            const i32x2 w1 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                                           (lds_s16x4*)(lds_char*)(v_at(r + 16, c) + b8)));
-            vf = i32x4{w0[0], w0[1], w1[0], w1[1]};
-          }
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) o[q][dt] = mfma16<F16>(vf, pf[q], o[q][dt]);
+      auto value = [&](int dt) {
+        if constexpr (KV8) {
+          const int r8 = col >> 1;
+          const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(lds_char*)(
+              v_at((r8 & 3) + 4 * grp + (r8 >> 2) * 16, dt) + (col & 1) * 8));
+          return widen8<F16>(w[0], w[1]);
+        } else {
+          const int r = 4 * grp + (col >> 2), c = 2 * dt + ((col & 3) >> 1), b8 = (col & 1) * 8;
+          const i32x2 w0 = __builtin_bit_cast(
+              i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)(v_at(r, c) + b8)));
+          const i32x2 w1 = __builtin_bit_cast(
+              i32x2,
+              __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)(v_at(r + 16, c) + b8)));
+          return i32x4{w0[0], w0[1], w1[0], w1[1]};
         }
+      };
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        i32x4 vf = value(dt);
+        if (odd) {
+#pragma unroll 1
+          for (int kind = 0; kind < 3; ++kind)
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              const f32x4 t = mfma16<F16>(where_kind<F16>(vf, kind), pf[q], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[q][dt][i] += t[i] > 0.f ? kind_value(kind) : 0.f;
+            }
+          vf = finite_part<F16>(vf);
+        }
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) o[q][dt] = mfma16<F16>(vf, pf[q], o[q][dt]);
       }
       __builtin_amdgcn_wave_barrier();  // read before the next block's are written
     }
@@ -527,14 +555,17 @@ template <int D> __device__ inline int v_off(int row, int chunk) {
   return row * (D * 2) + ((chunk ^ ((row << 1) & (D / 8 - 1))) << 4);
 }
 
-// Positions of a tile.
-template <int D> constexpr int tile_positions() { return 8192 / D; }
+// Positions of a tile: what leaves the registers of two waves per SIMD room
+// for the tile that is on its way (one wave per SIMD for dim 256).
+template <int D, int NW> constexpr int tile_positions() {
+  return D == 256 ? 32 : NW * 1024 / D;
+}
 
 // NW waves of 32 rows.  S^T tiles are 32x32 (MFMA 32x32x16): lane l holds row
 // l % 32 and positions 8 b + 4 (l / 32) + 0..3 of each.
 template <int D, int NW, bool F16, bool KV8>
 __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void tile_kernel(AttnArgs a) {
-  constexpr int BM = 32 * NW, BN = tile_positions<D>(), TH = NW * 64;
+  constexpr int BM = 32 * NW, BN = tile_positions<D, NW>(), TH = NW * 64;
   constexpr int NS = BN / 32;
   constexpr int DT = D / 32, KS = D / 16;
   constexpr int ES = KV8 ? 1 : 2;
@@ -553,8 +584,12 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void tile_kernel(AttnArg
   const int* const table = a.table + (int64_t)j.b * a.table_stride;
   const char* const kb = (const char*)a.k + j.hk * a.k_hs * ES;
   const char* const vb = (const char*)a.v + j.hk * a.v_hs * ES;
-  const int64_t k_ps = a.k_ps * ES, k_ts = a.k_ts * ES, v_ps = a.v_ps * ES, v_ts = a.v_ts * ES;
+  // a page's bytes fit 32 bits (checked on the host), a cache's need not
+  const uint32_t k_ps = a.k_ps * ES, k_ts = a.k_ts * ES, v_ps = a.v_ps * ES, v_ts = a.v_ts * ES;
   const int nrows = j.n * a.G;
+  // Two waves share a SIMD: one goes first, so that its products run while
+  // the other is at its exponentials, and the other way round.
+  if (wave >= 4) __builtin_amdgcn_s_setprio(1);
 
   for (int tile = j.tile0; tile * BM < nrows; tile += a.ntiles) {
     const int row0 = tile * BM;
@@ -591,16 +626,17 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void tile_kernel(AttnArg
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int pos = min(lo + it * BN + (tid + i * TH) / CPR, hi - 1);
-        pg[i] = min(max(table[pos >> a.page_log], 0), a.pages - 1);
+        pg[i] = table[pos >> a.page_log];  // not looked at before it is used: no wait here
       }
     };
     auto load_tile = [&](int it) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int idx = tid + i * TH;
+        const uint32_t page = min(max(pg[i], 0), a.pages - 1);
         const int in = min(lo + it * BN + idx / CPR, hi - 1) & a.page_mask;
-        rk[i] = *(const i32x4*)(kb + pg[i] * k_ps + in * k_ts + (idx % CPR) * 16);
-        rv[i] = *(const i32x4*)(vb + pg[i] * v_ps + in * v_ts + (idx % CPR) * 16);
+        rk[i] = *(const i32x4*)(kb + (uint64_t)page * k_ps + (in * k_ts + (idx % CPR) * 16));
+        rv[i] = *(const i32x4*)(vb + (uint64_t)page * v_ps + (in * v_ts + (idx % CPR) * 16));
       }
     };
     // Stores the loaded tile; says whether drafted values of it that some
@@ -639,102 +675,133 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void tile_kernel(AttnArg
     load_tile(0);
     if (ntl > 1) load_pages(1);
     bool odd = store_tile(0);
-    for (int it = 0; it < ntl; ++it) {
+    // One tile; TAIL: with positions that some rows do not see.
+    auto step = [&](int it, auto tail_tag) {
+      constexpr bool TAIL = decltype(tail_tag)::value;
       const int base = lo + it * BN;
-      const bool tail = base + BN > min(j.ctx, hi);
       const char* const sk = smem + (it & 1) * 2 * TILE;
       const char* const sv = sk + TILE;
       if (it + 1 < ntl) {
         load_tile(it + 1);
         if (it + 2 < ntl) load_pages(it + 2);
       }
-      f32x16 p[NS];
 #pragma unroll
       for (int ns = 0; ns < NS; ++ns) {
+        f32x16 p;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) p[ns][i] = 0.f;
+        for (int i = 0; i < 16; ++i) p[i] = 0.f;
+        // key fragments run a few ahead of the products that use them
+        constexpr int KA = 4;
+        i32x4 kf[KS];
+        auto key = [&](int f) {
+          return *(const i32x4*)(sk + k_off<D>(ns * 32 + col, 2 * f + half));
+        };
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const i32x4 kf = *(const i32x4*)(sk + k_off<D>(ns * 32 + col, 2 * ks + half));
-          p[ns] = mfma32<F16>(kf, qf[ks], p[ns]);
+        for (int f = 0; f < KA; ++f) kf[f] = key(f);
+#pragma unroll
+        for (int f = 0; f < KS; ++f) {
+          p = mfma32<F16>(kf[f], qf[f], p);
+          if (f + KA < KS) kf[f + KA] = key(f + KA);
         }
-      }
-      if (tail) {
+        __builtin_amdgcn_sched_group_barrier(0x100, KA, 0);
 #pragma unroll
-        for (int ns = 0; ns < NS; ++ns)
+        for (int f = 0; f < KS - KA; ++f) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, KA, 0);
+        if constexpr (TAIL) {
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             const uint32_t vis = sees4(a, j, node, mrow, base + ns * 32 + 8 * b + 4 * half, hi);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) p[ns][b * 4 + i] = (vis >> i) & 1 ? p[ns][b * 4 + i] : NEG_INF;
+            for (int i = 0; i < 4; ++i) p[b * 4 + i] = (vis >> i) & 1 ? p[b * 4 + i] : NEG_INF;
           }
-      }
-      float mx = p[0][0];
+        }
+        float mx = p[0];
 #pragma unroll
-      for (int i = 1; i < NS * 16; ++i) mx = fmaxf(mx, p[i >> 4][i & 15]);
-      const float mn = fmaxf(m, half_max(mx));
-      if (__any((mn - m) * j.sc > SLACK)) {
-        const float f = mn == NEG_INF ? 1.f : exp2_fast((m - mn) * j.sc);
-        m = mn;
-        l *= f;
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, p[i]);
+        const float mn = fmaxf(m, half_max(mx));
+        if (__any((mn - m) * j.sc > SLACK)) {
+          const float f = mn == NEG_INF ? 1.f : exp2_fast((m - mn) * j.sc);
+          m = mn;
+          l *= f;
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
+          for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[dt][i] *= f;
-      }
-      const float ms = m == NEG_INF ? 0.f : m * j.sc;
-      float sum = 0.f;
+            for (int i = 0; i < 16; ++i) o[dt][i] *= f;
+        }
+        const float ms = m == NEG_INF ? 0.f : m * j.sc;
+        float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < NS * 16; ++i) {
-        p[i >> 4][i & 15] = exp2_fast(fmaf(p[i >> 4][i & 15], j.sc, -ms));
-        sum += p[i >> 4][i & 15];
-      }
-      l += sum;
-      if (odd) {
-        // One position at a time: a weight of zero adds nothing, whatever
-        // the value there is.
+        for (int i = 0; i < 16; ++i) {
+          p[i] = exp2_fast(fmaf(p[i], j.sc, -ms));
+          sum += p[i];
+        }
+        l += sum;
+        i32x4 pf[2];  // rounded to the value type
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll 1
-          for (int r = 0; r < BN; ++r) {
-            float w = 0.f;
+        for (int tt = 0; tt < 2; ++tt)
 #pragma unroll
-            for (int i = 0; i < NS * 16; ++i)
-              if ((r >> 5) * 16 + ((r & 31) >> 3) * 4 + (r & 3) == i) w = p[i >> 4][i & 15];
-            w = __shfl(w, col + ((r >> 2) & 1) * 32);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int d = dt * 32 + (i >> 2) * 8 + half * 4 + (i & 3);
-              const float v =
-                  h_to_f32<F16>(*(const uint16_t*)(sv + v_off<D>(r, d >> 3) + (d & 7) * 2));
-              if (w != 0.f) o[dt][i] += w * v;
-            }
-          }
-      } else {
+          for (int w = 0; w < 4; ++w) pf[tt][w] = pack2<F16>(p[8 * tt + 2 * w], p[8 * tt + 2 * w + 1]);
         const int i16 = lane & 15;
         const int vr = 4 * half + (i16 >> 2);
         const int vc = 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
-#pragma unroll
-        for (int tt = 0; tt < 2 * NS; ++tt) {
-          i32x4 pf;  // sixteen positions' probabilities, rounded to the value type
-#pragma unroll
-          for (int w = 0; w < 4; ++w)
-            pf[w] = pack2<F16>(p[tt >> 1][8 * (tt & 1) + 2 * w], p[tt >> 1][8 * (tt & 1) + 2 * w + 1]);
+        // value fragments (two transposing reads each) run ahead likewise
+        constexpr int NF = 2 * DT, VA = NF < 4 ? NF : 4;
+        auto value = [&](int f) {
+          const int r = ns * 32 + vr + 16 * (f / DT), c = vc + 4 * (f % DT), b8 = (i16 & 1) * 8;
+          const i32x2 w0 = __builtin_bit_cast(
+              i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                         (lds_s16x4*)(lds_char*)(sv + v_off<D>(r, c) + b8)));
+          const i32x2 w1 = __builtin_bit_cast(
+              i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                         (lds_s16x4*)(lds_char*)(sv + v_off<D>(r + 8, c) + b8)));
+          return i32x4{w0[0], w0[1], w1[0], w1[1]};
+        };
+        if (TAIL && odd) {
 #pragma unroll
           for (int dt = 0; dt < DT; ++dt) {
-            const i32x2 w0 = __builtin_bit_cast(
-                i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)(
-                           sv + v_off<D>(vr + 16 * tt, vc + 4 * dt) + (i16 & 1) * 8)));
-            const i32x2 w1 = __builtin_bit_cast(
-                i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds_char*)(
-                           sv + v_off<D>(vr + 16 * tt + 8, vc + 4 * dt) + (i16 & 1) * 8)));
-            o[dt] = mfma32<F16>(i32x4{w0[0], w0[1], w1[0], w1[1]}, pf, o[dt]);
+#pragma unroll 1
+            for (int kind = 0; kind < 3; ++kind) {
+              f32x16 t;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) t[i] = 0.f;
+#pragma unroll
+              for (int tt = 0; tt < 2; ++tt)
+                t = mfma32<F16>(where_kind<F16>(value(tt * DT + dt), kind), pf[tt], t);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[dt][i] += t[i] > 0.f ? kind_value(kind) : 0.f;
+            }
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+              o[dt] = mfma32<F16>(finite_part<F16>(value(tt * DT + dt)), pf[tt], o[dt]);
           }
+        } else {
+          i32x4 vf[NF];
+#pragma unroll
+          for (int f = 0; f < VA; ++f) vf[f] = value(f);
+#pragma unroll
+          for (int f = 0; f < NF; ++f) {
+            o[f % DT] = mfma32<F16>(vf[f], pf[f / DT], o[f % DT]);
+            if (f + VA < NF) vf[f + VA] = value(f + VA);
+          }
+          __builtin_amdgcn_sched_group_barrier(0x100, 2 * VA, 1);
+#pragma unroll
+          for (int f = 0; f < NF - VA; ++f) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
+          }
+          __builtin_amdgcn_sched_group_barrier(0x008, VA, 1);
         }
       }
       // The other buffer was last read before the previous barrier.
       if (it + 1 < ntl) odd = store_tile(it + 1);
-    }
+    };
+    const int full = max(0, (min(j.ctx, hi) - lo) / BN);  // tiles that every row sees whole
+    int it = 0;
+    for (; it < full; ++it) step(it, std::false_type{});
+    for (; it < ntl; ++it) step(it, std::true_type{});
 
     l = half_sum(l);
     m *= j.sc;
@@ -822,7 +889,7 @@ hipError_t launch_one(const AttnArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((stream_kernel<D, NQ, F16, KV8>), dim3((unsigned)grid), dim3(256), lds, s, a);
   } else {
     constexpr int NW = SHAPE == AT_TILE128 ? 4 : 8;
-    constexpr size_t lds = tile_positions<D>() * D * 8;
+    constexpr size_t lds = tile_positions<D, NW>() * D * 8;
     e = opt_in_lds((const void*)tile_kernel<D, NW, F16, KV8>, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((tile_kernel<D, NW, F16, KV8>), dim3((unsigned)grid), dim3(NW * 64), lds, s,
