@@ -32,6 +32,8 @@
 
 #include "launch.hpp"
 
+#define ALWAYS_INLINE __attribute__((always_inline))
+
 namespace lg {
 namespace {
 
@@ -555,24 +557,425 @@ template <int D> __device__ inline int v_off(int row, int chunk) {
   return row * (D * 2) + ((chunk ^ ((row << 1) & (D / 8 - 1))) << 4);
 }
 
-// Positions of a tile: what leaves the registers of two waves per SIMD room
-// for the tile that is on its way (one wave per SIMD for dim 256).
-template <int D, int NW> constexpr int tile_positions() {
-  return D == 256 ? 32 : NW * 1024 / D;
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
+
+// The value fragment f of a block of 32 positions that starts at row `r0` of
+// a tile: sixteen positions (f / DT) by 32 values (f % DT), by two transposing
+// reads per lane.
+template <int D> __device__ inline i32x4 value_frag(const char* sv, int r0, int f, int lane) {
+  constexpr int DT = D / 32;
+  const int i16 = lane & 15;
+  const int r = r0 + 16 * (f / DT) + 4 * (lane >> 5) + (i16 >> 2);
+  const int c = 4 * (f % DT) + 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
+  const int b8 = (i16 & 1) * 8;
+  const i32x2 w0 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                 (lds_s16x4*)(lds_char*)(sv + v_off<D>(r, c) + b8)));
+  const i32x2 w1 =
+      __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                    (lds_s16x4*)(lds_char*)(sv + v_off<D>(r + 8, c) + b8)));
+  return i32x4{w0[0], w0[1], w1[0], w1[1]};
 }
 
-// NW waves of 32 rows.  S^T tiles are 32x32 (MFMA 32x32x16): lane l holds row
-// l % 32 and positions 8 b + 4 (l / 32) + 0..3 of each.
-template <int D, int NW, bool F16, bool KV8>
-__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void tile_kernel(AttnArgs a) {
-  constexpr int BM = 32 * NW, BN = tile_positions<D, NW>(), TH = NW * 64;
-  constexpr int NS = BN / 32;
-  constexpr int DT = D / 32, KS = D / 16;
+__device__ inline void clear(f32x16& p) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) p[i] = 0.f;
+}
+
+// One wave's 32 rows: what the tile kernels keep of them.
+template <int D, bool F16> struct Rows {
+  static constexpr int DT = D / 32, KS = D / 16;
+  i32x4 q[KS];
+  f32x16 o[DT];
+  float m, l;
+
+  // Scores of a block of 32 positions.  Key fragments are read a few ahead of
+  // the products that use them.
+  __device__ inline ALWAYS_INLINE void scores(f32x16& p, const char* sk, int r0, int lane) {
+    constexpr int KA = 4;
+    const int col = lane & 31, half = lane >> 5;
+    i32x4 kf[KS];
+    clear(p);
+#pragma unroll
+    for (int f = 0; f < KA; ++f) kf[f] = *(const i32x4*)(sk + k_off<D>(r0 + col, 2 * f + half));
+#pragma unroll
+    for (int f = 0; f < KS; ++f) {
+      p = mfma32<F16>(kf[f], q[f], p);
+      if (f + KA < KS) kf[f + KA] = *(const i32x4*)(sk + k_off<D>(r0 + col, 2 * (f + KA) + half));
+    }
+  }
+  // Masks (for the positions pos + ... of the block), running maximum and sum;
+  // p becomes the probabilities, rounded to the value type, in pf.
+  template <bool TAIL>
+  __device__ inline ALWAYS_INLINE void softmax(f32x16& p, i32x4 (&pf)[2], const AttnArgs& a,
+                                               const Job& j, int node, const int64_t* mrow, int pos,
+                                               int hi, int lane) {
+    if constexpr (TAIL) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t vis = sees4(a, j, node, mrow, pos + 8 * b + 4 * (lane >> 5), hi);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[b * 4 + i] = (vis >> i) & 1 ? p[b * 4 + i] : NEG_INF;
+      }
+    }
+    float mx = p[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) mx = fmaxf(mx, p[i]);
+    const float mn = fmaxf(m, half_max(mx));
+    if (__any((mn - m) * j.sc > SLACK)) {
+      const float f = mn == NEG_INF ? 1.f : exp2_fast((m - mn) * j.sc);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[dt][i] *= f;
+    }
+    const float ms = m == NEG_INF ? 0.f : m * j.sc;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      p[i] = exp2_fast(fmaf(p[i], j.sc, -ms));
+      sum += p[i];
+    }
+    l += sum;
+#pragma unroll
+    for (int tt = 0; tt < 2; ++tt)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) pf[tt][w] = pack2<F16>(p[8 * tt + 2 * w], p[8 * tt + 2 * w + 1]);
+  }
+  // O^T += V^T P^T for the block.  TAIL: values that some rows do not see, or
+  // that lie past the end, may be infinite or NaN.
+  template <bool TAIL>
+  __device__ inline ALWAYS_INLINE void values(const i32x4 (&pf)[2], const char* sv, int r0, int lane) {
+    constexpr int NF = 2 * DT, VA = 4 < NF ? 4 : NF;
+    if constexpr (TAIL) {
+      bool odd = false;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) odd |= not_finite8<F16>(value_frag<D>(sv, r0, f, lane));
+      if (__any(odd)) {
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+#pragma unroll 1
+          for (int kind = 0; kind < 3; ++kind) {
+            f32x16 t;
+            clear(t);
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt)
+              t = mfma32<F16>(where_kind<F16>(value_frag<D>(sv, r0, tt * DT + dt, lane), kind),
+                              pf[tt], t);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[dt][i] += t[i] > 0.f ? kind_value(kind) : 0.f;
+          }
+#pragma unroll
+          for (int tt = 0; tt < 2; ++tt)
+            o[dt] = mfma32<F16>(finite_part<F16>(value_frag<D>(sv, r0, tt * DT + dt, lane)), pf[tt],
+                                o[dt]);
+        }
+        return;
+      }
+    }
+    i32x4 vf[NF];
+#pragma unroll
+    for (int f = 0; f < VA; ++f) vf[f] = value_frag<D>(sv, r0, f, lane);
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      o[f % DT] = mfma32<F16>(vf[f], pf[f / DT], o[f % DT]);
+      if (f + VA < NF) vf[f + VA] = value_frag<D>(sv, r0, f + VA, lane);
+    }
+  }
+  // Writes a finished row, or its part of a split one.
+  __device__ inline void write(const AttnArgs& a, const Job& j, int64_t r, bool whole, int half) {
+    if (whole) {
+      const float inv = inverse_sum(l, a.v_scale ? a.v_scale[j.hk] : 1.f);
+      uint16_t* const op = a.out + r * D + half * 4;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          *(i32x2*)(op + dt * 32 + b * 8) =
+              i32x2{pack2<F16>(o[dt][b * 4] * inv, o[dt][b * 4 + 1] * inv),
+                    pack2<F16>(o[dt][b * 4 + 2] * inv, o[dt][b * 4 + 3] * inv)};
+      if (a.lse && half == 0) a.lse[r] = row_lse(m, l);
+    } else {
+      const int64_t pr = (int64_t)j.split * a.rows + r;
+      float* const op = a.part_o + pr * D + half * 4;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          *(f32x4*)(op + dt * 32 + b * 8) =
+              f32x4{o[dt][b * 4], o[dt][b * 4 + 1], o[dt][b * 4 + 2], o[dt][b * 4 + 3]};
+      if (half == 0) *(float2*)(a.part_ml + pr * 2) = make_float2(m, l);
+    }
+  }
+};
+
+// s_waitcnt immediate for "vmcnt <= n" (other counters not waited for).
+constexpr int vmcnt_imm(int n) { return (n & 15) | 0x0F70 | ((n >> 4) << 14); }
+
+// x, as a value of its own: what is computed from it is not kept in registers
+// over a loop that has better use for them.
+__device__ inline int again(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// A barrier that waits for nothing but the other waves.
+__device__ inline void phase_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Positions of a tile, and buffers of the tile kernel: 128 KB of LDS.
+template <int D> constexpr int tile_positions() { return 8192 / D; }
+constexpr int TILE_BUFS = 4;
+template <int D> constexpr int tile_lds_bytes() { return TILE_BUFS * tile_positions<D>() * D * 4; }
+
+// Eight waves of 32 rows.  S^T tiles are 32x32 (MFMA 32x32x16): lane l holds
+// row l % 32 and positions 8 b + 4 (l / 32) + 0..3 of each.  CW = 1: 256 rows;
+// CW = 2: 128 rows, waves 4..7 take the second half of each tile's positions
+// and their sums are joined at the end.
+//
+// The two waves of a SIMD alternate: while one runs the products of a block
+// (values of this one, keys of the next) the other runs its softmax, in
+// phases between barriers, waves 4..7 one phase behind waves 0..3.  With NB
+// blocks per wave and tile, wave group g has the softmax of block k of tile
+// it in phase 2 NB it + 2 k + g and its products in the next.  So
+//  - tile it - 1 is last read in phase 2 NB it, and its buffer is refilled
+//    (with tile it + 3) from the next phase on;
+//  - tile it + 1 is first read in phase 2 NB it + 2 NB - 1: every wave has
+//    waited for its own loads of it by the end of the phase before.
+// 16-bit caches go from memory to LDS directly, three tiles ahead; 8-bit
+// codes pass through registers, where they are widened.
+template <int D, int CW, bool F16, bool KV8>
+__global__ __launch_bounds__(512) void tile_kernel(AttnArgs a) {
+  constexpr int BM = 256 / CW, BN = tile_positions<D>();
+  constexpr int NB = BN / 32 / CW;
   constexpr int ES = KV8 ? 1 : 2;
   constexpr int CPR = D * ES / 16;       // 16-byte chunks of a cache row
-  constexpr int NI = BN * CPR / TH;      // chunks per thread, tile and operand
+  constexpr int NI = BN * CPR / 512;     // chunks per thread, tile and operand
   constexpr int TILE = BN * D * 2;       // bytes of one operand's tile
-  static_assert(NI * TH == BN * CPR, "whole chunks per thread");
+  static_assert(NI * 512 == BN * CPR, "whole chunks per thread");
+
+  extern __shared__ __align__(16) char smem[];  // [TILE_BUFS][keys, values]
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = lane >> 5, col = lane & 31;
+  const int grp = wave >> 2, rw = CW == 1 ? wave : wave & 3, b0 = CW == 1 ? 0 : grp * NB;
+
+  Job j;
+  if (!find_job(a, j)) return;
+  const int* const table = a.table + (int64_t)j.b * a.table_stride;
+  const char* const kb = (const char*)a.k + j.hk * a.k_hs * ES;
+  const char* const vb = (const char*)a.v + j.hk * a.v_hs * ES;
+  // a page's bytes fit 32 bits (checked on the host), a cache's need not
+  const uint32_t k_ps = a.k_ps * ES, k_ts = a.k_ts * ES, v_ps = a.v_ps * ES, v_ts = a.v_ts * ES;
+  const int nrows = j.n * a.G;
+  if (grp) __builtin_amdgcn_s_setprio(1);
+
+  for (int tile = j.tile0; tile * BM < nrows; tile += a.ntiles) {
+    const int row0 = tile * BM;
+    const int last = min(row0 + BM - 1, nrows - 1) / a.G;
+    int lo, hi;
+    const int nsp = split_range(a, j, last, lo, hi);
+    if (j.split >= nsp) continue;
+    const int ntl = (hi - lo + BN - 1) / BN;
+    // tiles that every row sees whole
+    const int all = min(a.mask ? j.ctx : j.ctx + row0 / a.G + 1, hi);
+    const int full = max(0, (all - lo) / BN);
+
+    // this lane's row (rows past the end stand for the first and are not stored)
+    struct Row { bool live; int node, head; };
+    auto my_row = [&]() ALWAYS_INLINE {
+      const int row = row0 + rw * 32 + (again(lane) & 31);
+      const bool live = row < nrows;
+      const int node = live ? row / a.G : 0;
+      return Row{live, node, j.hk * a.G + (live ? row - node * a.G : 0)};
+    };
+    Rows<D, F16> w;
+    {
+      const Row r = my_row();
+      const uint16_t* qp = a.q + (int64_t)(j.t0 + r.node) * a.q_ts + r.head * a.q_hs + half * 8;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        w.q[ks] = scaled_q(*(const i32x4*)(qp + ks * 16), j.flip, j.none || !r.live);
+    }
+    w.m = NEG_INF;
+    w.l = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt) clear(w.o[dt]);
+
+    // The cache rows that this thread loads of a tile: chunk idx of the tile
+    // in LDS order is row idx / CPR (and, loaded directly, holds the chunk
+    // that the XOR puts there).
+    auto chunk_row = [&](int i, int ln) ALWAYS_INLINE { return ((wave * NI + i) * 64 + ln) / CPR; };
+    struct Pages { int p[NI]; };
+    auto load_pages = [&](int it) ALWAYS_INLINE {
+      Pages g;
+      const int ln = again(lane);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        g.p[i] = table[min(lo + it * BN + chunk_row(i, ln), hi - 1) >> a.page_log];
+      return g;  // not looked at before it is used: no wait here
+    };
+    auto buffer = [&](int it) ALWAYS_INLINE { return smem + (it % TILE_BUFS) * 2 * TILE; };
+    i32x4 rk[NI], rv[NI];  // 8-bit caches
+    auto issue = [&](int it, const Pages& g) ALWAYS_INLINE {
+      char* const sk = buffer(it);
+      const int ln = again(lane);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = chunk_row(i, ln), c = ln % CPR;
+        const uint32_t page = min(max(g.p[i], 0), a.pages - 1);
+        const int in = min(lo + it * BN + r, hi - 1) & a.page_mask;
+        const char* ka = kb + (uint64_t)page * k_ps + in * k_ts;
+        const char* va = vb + (uint64_t)page * v_ps + in * v_ts;
+        if constexpr (KV8) {
+          rk[i] = *(const i32x4*)(ka + c * 16);
+          rv[i] = *(const i32x4*)(va + c * 16);
+        } else {
+          char* const at = sk + (wave * NI + i) * 1024;
+          __builtin_amdgcn_global_load_lds((global_void*)(ka + ((c ^ (r & (CPR - 1))) << 4)),
+                                           (lds_void*)at, 16, 0, 0);
+          __builtin_amdgcn_global_load_lds((global_void*)(va + ((c ^ ((r << 1) & (CPR - 1))) << 4)),
+                                           (lds_void*)(at + TILE), 16, 0, 0);
+        }
+      }
+    };
+    // 8-bit: widen what was loaded into its buffer.
+    auto store = [&](int it) ALWAYS_INLINE {
+      char* const sk = buffer(it);
+      char* const sv = sk + TILE;
+      const int ln = again(lane);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = chunk_row(i, ln), c = ln % CPR;
+        *(i32x4*)(sk + k_off<D>(r, 2 * c)) = widen8<F16>(rk[i][0], rk[i][1]);
+        *(i32x4*)(sk + k_off<D>(r, 2 * c + 1)) = widen8<F16>(rk[i][2], rk[i][3]);
+        *(i32x4*)(sv + v_off<D>(r, 2 * c)) = widen8<F16>(rv[i][0], rv[i][1]);
+        *(i32x4*)(sv + v_off<D>(r, 2 * c + 1)) = widen8<F16>(rv[i][2], rv[i][3]);
+      }
+    };
+    Pages pg;
+    // Tile `it` is in LDS as far as this wave loads it.  `behind`: tiles whose
+    // loads were issued after its own (16-bit), if all of them were.
+    auto finish = [&](int it, int behind) ALWAYS_INLINE {
+      if (it >= ntl) return;
+      if constexpr (KV8) {
+        store(it);
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): written
+        if (it + 1 < ntl) {
+          issue(it + 1, pg);
+          if (it + 2 < ntl) pg = load_pages(it + 2);
+        }
+      } else if (it + behind >= ntl) {
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+      } else if (behind == 2) {
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(4 * NI));
+      } else {
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * NI));
+      }
+    };
+
+    if constexpr (KV8) {
+      pg = load_pages(0);
+      issue(0, pg);
+      if (ntl > 1) pg = load_pages(1);
+      finish(0, 0);
+
+    } else {
+      const Pages g0 = load_pages(0), g1 = load_pages(1), g2 = load_pages(2);
+      pg = load_pages(3);
+      issue(0, g0);
+      if (ntl > 1) issue(1, g1);
+      if (ntl > 2) issue(2, g2);
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    }
+    __syncthreads();
+
+    f32x16 p;
+    i32x4 pf[2];
+    const bool busy = row0 + rw * 32 < nrows;  // any live row in this wave
+    w.scores(p, buffer(0), b0 * 32, lane);
+    auto step = [&](int it, auto tail_tag) ALWAYS_INLINE {
+      constexpr bool TAIL = decltype(tail_tag)::value;
+      const char* const sk = buffer(it);
+      if (!KV8 && it + 3 < ntl) {
+        issue(it + 3, pg);
+        pg = load_pages(it + 4);
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        if (busy) {
+          int node = 0;
+          const int64_t* mrow = nullptr;
+          if constexpr (TAIL) {
+            node = my_row().node;
+            if (a.mask) mrow = a.mask + (int64_t)(j.t0 + node) * a.mask_words;
+          }
+          w.template softmax<TAIL>(p, pf, a, j, node, mrow, lo + it * BN + (b0 + k) * 32, hi, lane);
+          w.template values<TAIL>(pf, sk + TILE, (b0 + k) * 32, lane);
+          if (k + 1 < NB) w.scores(p, sk, (b0 + k + 1) * 32, lane);
+        }
+      }
+      finish(it + 1, 2);
+      phase_barrier();
+      // (past the last block: of whatever the next buffer holds, not used)
+      if (busy) w.scores(p, buffer(it + 1), b0 * 32, lane);
+    };
+    int it = 0;
+    for (; it < full; ++it) step(it, std::false_type{});
+    for (; it < ntl; ++it) step(it, std::true_type{});
+    __syncthreads();
+
+    w.l = half_sum(w.l);
+    w.m *= j.sc;
+    if constexpr (CW == 2) {
+      // the second halves' sums go to the first through LDS
+      float* const st = (float*)(smem + 4 * 32 * D * 4);  // [4][32][2]
+      f32x4* const sums = (f32x4*)smem + rw * (32 * D / 4);
+      if (grp == 1) {
+        if (half == 0) *(float2*)(st + (rw * 32 + col) * 2) = make_float2(w.m, w.l);
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            sums[(dt * 4 + b) * 64 + lane] =
+                f32x4{w.o[dt][b * 4], w.o[dt][b * 4 + 1], w.o[dt][b * 4 + 2], w.o[dt][b * 4 + 3]};
+      }
+      __syncthreads();
+      if (grp == 0) {
+        const float2 ml = *(const float2*)(st + (rw * 32 + col) * 2);
+        const float M = fmaxf(w.m, ml.x), ms = M == NEG_INF ? 0.f : M;
+        const float f0 = exp2_fast(w.m - ms), f1 = exp2_fast(ml.x - ms);
+        w.m = M;
+        w.l = w.l * f0 + ml.y * f1;
+#pragma unroll
+        for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) {
+            const f32x4 x = sums[(dt * 4 + b) * 64 + lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w.o[dt][b * 4 + i] = w.o[dt][b * 4 + i] * f0 + x[i] * f1;
+          }
+      }
+    }
+    const Row r = my_row();
+    if (r.live && (CW == 1 || grp == 0))
+      w.write(a, j, (int64_t)(j.t0 + r.node) * (a.Hk * a.G) + r.head, nsp == 1, half);
+    __syncthreads();  // smem is written again for the next row tile
+  }
+}
+
+// dim 256: O and Q of 32 rows take most of the registers of one wave per SIMD.
+// Four waves, tiles of 32 positions through registers into two buffers.
+template <bool F16, bool KV8>
+__global__ __launch_bounds__(256) void wide_kernel(AttnArgs a) {
+  constexpr int D = 256, BM = 128, BN = 32;
+  constexpr int ES = KV8 ? 1 : 2;
+  constexpr int CPR = D * ES / 16, NI = BN * CPR / 256, TILE = BN * D * 2;
 
   extern __shared__ __align__(16) char smem[];  // [2][keys, values]
   const int tid = threadIdx.x, lane = tid & 63;
@@ -584,12 +987,8 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void tile_kernel(AttnArg
   const int* const table = a.table + (int64_t)j.b * a.table_stride;
   const char* const kb = (const char*)a.k + j.hk * a.k_hs * ES;
   const char* const vb = (const char*)a.v + j.hk * a.v_hs * ES;
-  // a page's bytes fit 32 bits (checked on the host), a cache's need not
   const uint32_t k_ps = a.k_ps * ES, k_ts = a.k_ts * ES, v_ps = a.v_ps * ES, v_ts = a.v_ts * ES;
   const int nrows = j.n * a.G;
-  // Two waves share a SIMD: one goes first, so that its products run while
-  // the other is at its exponentials, and the other way round.
-  if (wave >= 4) __builtin_amdgcn_s_setprio(1);
 
   for (int tile = j.tile0; tile * BM < nrows; tile += a.ntiles) {
     const int row0 = tile * BM;
@@ -598,64 +997,50 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void tile_kernel(AttnArg
     const int nsp = split_range(a, j, last, lo, hi);
     if (j.split >= nsp) continue;
     const int ntl = (hi - lo + BN - 1) / BN;
+    const int all = min(a.mask ? j.ctx : j.ctx + row0 / a.G + 1, hi);
+    const int full = max(0, (all - lo) / BN);
 
     const int row = row0 + wave * 32 + col;
     const bool live = row < nrows;
     const int node = live ? row / a.G : 0;
     const int64_t t = j.t0 + node;
     const int head = j.hk * a.G + (live ? row % a.G : 0);
-    i32x4 qf[KS];
+    const int64_t* const mrow = a.mask ? a.mask + t * a.mask_words : nullptr;
+    Rows<D, F16> w;
     {
       const uint16_t* qp = a.q + t * a.q_ts + head * a.q_hs + half * 8;
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-        qf[ks] = scaled_q(*(const i32x4*)(qp + ks * 16), j.flip, j.none || !live);
+      for (int ks = 0; ks < D / 16; ++ks)
+        w.q[ks] = scaled_q(*(const i32x4*)(qp + ks * 16), j.flip, j.none || !live);
     }
-    const int64_t* const mrow = a.mask ? a.mask + t * a.mask_words : nullptr;
-
-    float m = NEG_INF, l = 0.f;
-    f32x16 o[DT];
+    w.m = NEG_INF;
+    w.l = 0.f;
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[dt][i] = 0.f;
+    for (int dt = 0; dt < D / 32; ++dt) clear(w.o[dt]);
 
-    int pg[NI];  // pages of the rows this thread loads next
+    int pg[NI];
     i32x4 rk[NI], rv[NI];
-    auto load_pages = [&](int it) {
+    auto load_pages = [&](int it) ALWAYS_INLINE {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int pos = min(lo + it * BN + (tid + i * TH) / CPR, hi - 1);
-        pg[i] = table[pos >> a.page_log];  // not looked at before it is used: no wait here
-      }
+      for (int i = 0; i < NI; ++i)
+        pg[i] = table[min(lo + it * BN + (tid + i * 256) / CPR, hi - 1) >> a.page_log];
     };
-    auto load_tile = [&](int it) {
+    auto load_tile = [&](int it) ALWAYS_INLINE {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int idx = tid + i * TH;
+        const int r = (tid + i * 256) / CPR, c = tid % CPR;
         const uint32_t page = min(max(pg[i], 0), a.pages - 1);
-        const int in = min(lo + it * BN + idx / CPR, hi - 1) & a.page_mask;
-        rk[i] = *(const i32x4*)(kb + (uint64_t)page * k_ps + (in * k_ts + (idx % CPR) * 16));
-        rv[i] = *(const i32x4*)(vb + (uint64_t)page * v_ps + (in * v_ts + (idx % CPR) * 16));
+        const int in = min(lo + it * BN + r, hi - 1) & a.page_mask;
+        rk[i] = *(const i32x4*)(kb + (uint64_t)page * k_ps + (in * k_ts + c * 16));
+        rv[i] = *(const i32x4*)(vb + (uint64_t)page * v_ps + (in * v_ts + c * 16));
       }
     };
-    // Stores the loaded tile; says whether drafted values of it that some
-    // rows may not see hold an infinity or NaN (positions past the end are
-    // stored as zero).
-    auto store_tile = [&](int it) {
-      const int base = lo + it * BN;
-      const bool tail = base + BN > min(j.ctx, hi);
+    auto store_tile = [&](int it) ALWAYS_INLINE {
       char* const sk = smem + (it & 1) * 2 * TILE;
       char* const sv = sk + TILE;
-      bool odd = false;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int idx = tid + i * TH;
-        const int r = idx / CPR, c = idx % CPR;
-        if (tail) {
-          if (base + r >= hi) rk[i] = rv[i] = i32x4{0, 0, 0, 0};
-          else if (base + r >= j.ctx) odd |= KV8 ? nan_codes(rv[i]) : not_finite8<F16>(rv[i]);
-        }
+        const int r = (tid + i * 256) / CPR, c = tid % CPR;
         if constexpr (KV8) {
           *(i32x4*)(sk + k_off<D>(r, 2 * c)) = widen8<F16>(rk[i][0], rk[i][1]);
           *(i32x4*)(sk + k_off<D>(r, 2 * c + 1)) = widen8<F16>(rk[i][2], rk[i][3]);
@@ -666,170 +1051,34 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void tile_kernel(AttnArg
           *(i32x4*)(sv + v_off<D>(r, c)) = rv[i];
         }
       }
-      if (tail) return __syncthreads_or(odd) != 0;
       __syncthreads();
-      return false;
     };
-
     load_pages(0);
     load_tile(0);
     if (ntl > 1) load_pages(1);
-    bool odd = store_tile(0);
-    // One tile; TAIL: with positions that some rows do not see.
-    auto step = [&](int it, auto tail_tag) {
+    store_tile(0);
+    auto step = [&](int it, auto tail_tag) ALWAYS_INLINE {
       constexpr bool TAIL = decltype(tail_tag)::value;
-      const int base = lo + it * BN;
       const char* const sk = smem + (it & 1) * 2 * TILE;
-      const char* const sv = sk + TILE;
       if (it + 1 < ntl) {
         load_tile(it + 1);
         if (it + 2 < ntl) load_pages(it + 2);
       }
-#pragma unroll
-      for (int ns = 0; ns < NS; ++ns) {
-        f32x16 p;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) p[i] = 0.f;
-        // key fragments run a few ahead of the products that use them
-        constexpr int KA = 4;
-        i32x4 kf[KS];
-        auto key = [&](int f) {
-          return *(const i32x4*)(sk + k_off<D>(ns * 32 + col, 2 * f + half));
-        };
-#pragma unroll
-        for (int f = 0; f < KA; ++f) kf[f] = key(f);
-#pragma unroll
-        for (int f = 0; f < KS; ++f) {
-          p = mfma32<F16>(kf[f], qf[f], p);
-          if (f + KA < KS) kf[f + KA] = key(f + KA);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x100, KA, 0);
-#pragma unroll
-        for (int f = 0; f < KS - KA; ++f) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x008, KA, 0);
-        if constexpr (TAIL) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint32_t vis = sees4(a, j, node, mrow, base + ns * 32 + 8 * b + 4 * half, hi);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p[b * 4 + i] = (vis >> i) & 1 ? p[b * 4 + i] : NEG_INF;
-          }
-        }
-        float mx = p[0];
-#pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, p[i]);
-        const float mn = fmaxf(m, half_max(mx));
-        if (__any((mn - m) * j.sc > SLACK)) {
-          const float f = mn == NEG_INF ? 1.f : exp2_fast((m - mn) * j.sc);
-          m = mn;
-          l *= f;
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[dt][i] *= f;
-        }
-        const float ms = m == NEG_INF ? 0.f : m * j.sc;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          p[i] = exp2_fast(fmaf(p[i], j.sc, -ms));
-          sum += p[i];
-        }
-        l += sum;
-        i32x4 pf[2];  // rounded to the value type
-#pragma unroll
-        for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) pf[tt][w] = pack2<F16>(p[8 * tt + 2 * w], p[8 * tt + 2 * w + 1]);
-        const int i16 = lane & 15;
-        const int vr = 4 * half + (i16 >> 2);
-        const int vc = 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
-        // value fragments (two transposing reads each) run ahead likewise
-        constexpr int NF = 2 * DT, VA = NF < 4 ? NF : 4;
-        auto value = [&](int f) {
-          const int r = ns * 32 + vr + 16 * (f / DT), c = vc + 4 * (f % DT), b8 = (i16 & 1) * 8;
-          const i32x2 w0 = __builtin_bit_cast(
-              i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                         (lds_s16x4*)(lds_char*)(sv + v_off<D>(r, c) + b8)));
-          const i32x2 w1 = __builtin_bit_cast(
-              i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                         (lds_s16x4*)(lds_char*)(sv + v_off<D>(r + 8, c) + b8)));
-          return i32x4{w0[0], w0[1], w1[0], w1[1]};
-        };
-        if (TAIL && odd) {
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt) {
-#pragma unroll 1
-            for (int kind = 0; kind < 3; ++kind) {
-              f32x16 t;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) t[i] = 0.f;
-#pragma unroll
-              for (int tt = 0; tt < 2; ++tt)
-                t = mfma32<F16>(where_kind<F16>(value(tt * DT + dt), kind), pf[tt], t);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[dt][i] += t[i] > 0.f ? kind_value(kind) : 0.f;
-            }
-#pragma unroll
-            for (int tt = 0; tt < 2; ++tt)
-              o[dt] = mfma32<F16>(finite_part<F16>(value(tt * DT + dt)), pf[tt], o[dt]);
-          }
-        } else {
-          i32x4 vf[NF];
-#pragma unroll
-          for (int f = 0; f < VA; ++f) vf[f] = value(f);
-#pragma unroll
-          for (int f = 0; f < NF; ++f) {
-            o[f % DT] = mfma32<F16>(vf[f], pf[f / DT], o[f % DT]);
-            if (f + VA < NF) vf[f + VA] = value(f + VA);
-          }
-          __builtin_amdgcn_sched_group_barrier(0x100, 2 * VA, 1);
-#pragma unroll
-          for (int f = 0; f < NF - VA; ++f) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);
-          }
-          __builtin_amdgcn_sched_group_barrier(0x008, VA, 1);
-        }
-      }
-      // The other buffer was last read before the previous barrier.
-      if (it + 1 < ntl) odd = store_tile(it + 1);
+      f32x16 p;
+      i32x4 pf[2];
+      w.scores(p, sk, 0, lane);
+      w.template softmax<TAIL>(p, pf, a, j, node, mrow, lo + it * BN, hi, lane);
+      w.template values<TAIL>(pf, sk + TILE, 0, lane);
+      // the other buffer was last read before the previous barrier
+      if (it + 1 < ntl) store_tile(it + 1);
     };
-    const int full = max(0, (min(j.ctx, hi) - lo) / BN);  // tiles that every row sees whole
     int it = 0;
     for (; it < full; ++it) step(it, std::false_type{});
     for (; it < ntl; ++it) step(it, std::true_type{});
 
-    l = half_sum(l);
-    m *= j.sc;
-    if (live) {
-      const int64_t r = t * ((int64_t)a.Hk * a.G) + head;
-      if (nsp == 1) {
-        const float inv = inverse_sum(l, a.v_scale ? a.v_scale[j.hk] : 1.f);
-        uint16_t* const op = a.out + r * D + half * 4;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            *(i32x2*)(op + dt * 32 + b * 8) =
-                i32x2{pack2<F16>(o[dt][b * 4] * inv, o[dt][b * 4 + 1] * inv),
-                      pack2<F16>(o[dt][b * 4 + 2] * inv, o[dt][b * 4 + 3] * inv)};
-        if (a.lse && half == 0) a.lse[r] = row_lse(m, l);
-      } else {
-        const int64_t pr = (int64_t)j.split * a.rows + r;
-        float* const op = a.part_o + pr * D + half * 4;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            *(f32x4*)(op + dt * 32 + b * 8) =
-                f32x4{o[dt][b * 4], o[dt][b * 4 + 1], o[dt][b * 4 + 2], o[dt][b * 4 + 3]};
-        if (half == 0) *(float2*)(a.part_ml + pr * 2) = make_float2(m, l);
-      }
-    }
+    w.l = half_sum(w.l);
+    w.m *= j.sc;
+    if (live) w.write(a, j, t * ((int64_t)a.Hk * a.G) + head, nsp == 1, half);
     __syncthreads();  // smem is written again for the next row tile
   }
 }
@@ -887,13 +1136,17 @@ hipError_t launch_one(const AttnArgs& a, hipStream_t s) {
     e = opt_in_lds((const void*)stream_kernel<D, NQ, F16, KV8>, lds);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((stream_kernel<D, NQ, F16, KV8>), dim3((unsigned)grid), dim3(256), lds, s, a);
-  } else {
-    constexpr int NW = SHAPE == AT_TILE128 ? 4 : 8;
-    constexpr size_t lds = tile_positions<D, NW>() * D * 8;
-    e = opt_in_lds((const void*)tile_kernel<D, NW, F16, KV8>, lds);
+  } else if constexpr (D == 256) {
+    constexpr size_t lds = 2 * 2 * 32 * D * 2;
+    e = opt_in_lds((const void*)wide_kernel<F16, KV8>, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((tile_kernel<D, NW, F16, KV8>), dim3((unsigned)grid), dim3(NW * 64), lds, s,
-                       a);
+    hipLaunchKernelGGL((wide_kernel<F16, KV8>), dim3((unsigned)grid), dim3(256), lds, s, a);
+  } else {
+    constexpr int CW = SHAPE == AT_TILE128 ? 2 : 1;
+    constexpr size_t lds = tile_lds_bytes<D>();
+    e = opt_in_lds((const void*)tile_kernel<D, CW, F16, KV8>, lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((tile_kernel<D, CW, F16, KV8>), dim3((unsigned)grid), dim3(512), lds, s, a);
   }
   e = hipGetLastError();
   if (e != hipSuccess || a.nsplit == 1) return e;
@@ -943,7 +1196,7 @@ AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t m
     ns = std::min(ns, (steps + 1) / 2);
   } else {
     // as many as fill whole rounds best; splits of four tiles at least
-    const int64_t slots = p.shape == AT_TILE128 && D < 256 ? 512 : 256;
+    const int64_t slots = 256;
     double best = 0;
     ns = 1;
     for (int64_t n = 1; n <= std::min<int64_t>(16, (steps + 3) / 4); ++n) {
