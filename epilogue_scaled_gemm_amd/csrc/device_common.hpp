@@ -141,6 +141,18 @@ template <bool F16> __device__ inline uint16_t f32_to_h(float f) {
   return __builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
+// Two fp32 -> packed 16-bit floats (round to nearest even).
+template <bool F16> __device__ inline int pack2(float a, float b) {
+  typedef __attribute__((ext_vector_type(2))) float f32x2;
+  if constexpr (F16) {
+    typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
+    return __builtin_bit_cast(int, __builtin_convertvector((f32x2{a, b}), f16x2));
+  } else {
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+    return __builtin_bit_cast(int, __builtin_convertvector((f32x2{a, b}), bf16x2));
+  }
+}
+
 // ------------------------------------------- dynamic quantization helpers
 // A quantization group (a token row, or a 1x128 block of one) divides every
 // value by its scale s = max|x| / QMAX and rounds the binary32 quotient to a

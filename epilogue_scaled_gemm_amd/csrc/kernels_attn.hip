@@ -67,18 +67,6 @@ template <bool F16> __device__ inline f32x16 mfma32(i32x4 a, i32x4 b, f32x16 c) 
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Two fp32 -> packed 16-bit floats (round to nearest even).
-template <bool F16> __device__ inline int pack2(float a, float b) {
-  typedef __attribute__((ext_vector_type(2))) float f32x2;
-  if constexpr (F16) {
-    typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
-    return __builtin_bit_cast(int, __builtin_convertvector((f32x2{a, b}), f16x2));
-  } else {
-    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
-    return __builtin_bit_cast(int, __builtin_convertvector((f32x2{a, b}), bf16x2));
-  }
-}
-
 // Two e4m3 codes (bytes 2 HI and 2 HI + 1 of w) -> packed 16-bit floats, exact.
 template <bool F16, bool HI> __device__ inline int widen2(int w) {
   if constexpr (F16) {

@@ -20,23 +20,46 @@ namespace lg {
 namespace {
 
 constexpr int RP_THREADS = 256;
+constexpr int RP_WAVES = 4;
 
-// LPH lanes hold one head (the power of two at or above D / 8).
-template <bool F16, int LPH>
+// LPH lanes hold one head (the power of two at or above D / 8), a wave 64 / LPH
+// heads of one kind, so that everything that depends on the kind is scalar;
+// wave jobs of a token are its queries, keys and values in turn.  NPT jobs
+// per wave: their loads all go out first, and the token's cosines and sines
+// are read once for them.
+template <bool F16, int LPH, int NPT>
 __global__ __launch_bounds__(RP_THREADS) void heads_kernel(HeadArgs a) {
-  constexpr int GROUPS = RP_THREADS / LPH;
-  const int c = threadIdx.x % LPH;  // 16-byte chunk of the head
-  const int grp = threadIdx.x / LPH;
+  constexpr int HPW = 64 / LPH;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane % LPH, grp = lane / LPH;  // 16-byte chunk, head of the wave
   const int64_t t = blockIdx.x;
   const int nch = a.D >> 3;
-  const int heads = a.Hq + a.Hk + a.Hv;
+  const int jq = (a.Hq + HPW - 1) / HPW, jk = (a.Hk + HPW - 1) / HPW, jv = (a.Hv + HPW - 1) / HPW;
+  const int job0 = blockIdx.y * RP_WAVES + wave, step = gridDim.y * RP_WAVES;
+
+  i32x4 raw[NPT];
+  int kind[NPT], head[NPT];  // 0 query, 1 key, 2 value, 3 none
+#pragma unroll
+  for (int i = 0; i < NPT; ++i) {
+    const int job = job0 + i * step;
+    kind[i] = job < jq ? 0 : job < jq + jk ? 1 : job < jq + jk + jv ? 2 : 3;
+    const int count = kind[i] == 0 ? a.Hq : a.Hk;
+    head[i] = (kind[i] == 0 ? job : kind[i] == 1 ? job - jq : job - jq - jk) * HPW + grp;
+    if (head[i] >= count || c >= nch) head[i] = -1;
+    raw[i] = i32x4{0, 0, 0, 0};
+    if (kind[i] < 3 && head[i] >= 0) {
+      const HeadView& v = kind[i] == 0 ? a.q : kind[i] == 1 ? a.k : a.v;
+      raw[i] = *(const i32x4*)((const uint16_t*)v.p + t * v.ts + head[i] * v.hs + c * 8);
+    }
+  }
 
   // This lane's cosines and sines, the same for every head of the token.
   float cs[8], sn[8];
   const bool turns = a.table && c < (a.rot >> 3);
-  if (a.table) {
-    const int64_t pos = min(max(a.positions[t], 0), a.max_pos - 1);
-    const float* row = a.table + pos * a.rot;
+  if (a.table && job0 < jq + jk) {
+    const int pos = min(max(a.positions[t], 0), a.max_pos - 1);
+    const float* row = a.table + (int64_t)pos * a.rot;
     const int hr = a.rot >> 1;
     if (turns) {
       if (a.interleaved) {
@@ -70,107 +93,102 @@ __global__ __launch_bounds__(RP_THREADS) void heads_kernel(HeadArgs a) {
     in = slot & ((1 << a.page_log) - 1);
   }
 
-  for (int hh = blockIdx.y * GROUPS + grp; hh < heads; hh += gridDim.y * GROUPS) {
-    const int kind = hh < a.Hq ? 0 : hh < a.Hq + a.Hk ? 1 : 2;  // query, key, value
-    const int h = kind == 0 ? hh : kind == 1 ? hh - a.Hq : hh - a.Hq - a.Hk;
-    const HeadView& src = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
-    i32x4 raw = {0, 0, 0, 0};
-    if (c < nch) raw = *(const i32x4*)((const uint16_t*)src.p + t * src.ts + h * src.hs + c * 8);
+#pragma unroll
+  for (int i = 0; i < NPT; ++i) {
+    if (kind[i] == 3) break;
     float y[8];
-    unpack8<F16>(raw, y);
-    if (kind < 2) {
-      const uint16_t* w = kind == 0 ? a.q_weight : a.k_weight;
+    unpack8<F16>(raw[i], y);
+    if (kind[i] < 2) {
+      const uint16_t* w = kind[i] == 0 ? a.q_weight : a.k_weight;
       if (w) {
         float ss = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss += y[i] * y[i];
+        for (int e = 0; e < 8; ++e) ss += y[e] * y[e];
 #pragma unroll
         for (int off = LPH / 2; off > 0; off >>= 1) ss += __shfl_xor(ss, off, LPH);
-        const float r = 1.f / sqrtf(ss / (float)a.D + a.eps);
+        const float r = __builtin_amdgcn_rsqf(ss / (float)a.D + a.eps);
         float wf[8];
         i32x4 wr = {0, 0, 0, 0};
         if (c < nch) wr = *(const i32x4*)(w + c * 8);
         unpack8<F16>(wr, wf);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = y[i] * r * wf[i];
+        for (int e = 0; e < 8; ++e) y[e] = y[e] * r * wf[e];
       }
       if (a.table) {
         if (a.interleaved) {
           if (turns) {
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const float p = y[i], q = y[i + 1];
-              y[i] = p * cs[i] - q * sn[i];
-              y[i + 1] = q * cs[i] + p * sn[i];
+            for (int e = 0; e < 8; e += 2) {
+              const float p = y[e], q = y[e + 1];
+              y[e] = p * cs[e] - q * sn[e];
+              y[e + 1] = q * cs[e] + p * sn[e];
             }
           }
         } else {
           const int hc = a.rot >> 4;  // chunks of half the rotated part
           const bool lo = c < hc;
-          const int other = lo ? c + hc : c - hc;
+          const int other = !turns ? c : lo ? c + hc : c - hc;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float z = __shfl(y[i], turns ? other : c, LPH);
-            if (turns) y[i] = lo ? y[i] * cs[i] - z * sn[i] : y[i] * cs[i] + z * sn[i];
+          for (int e = 0; e < 8; ++e) {
+            const float z = __shfl(y[e], other, LPH);
+            if (turns) y[e] = lo ? y[e] * cs[e] - z * sn[e] : y[e] * cs[e] + z * sn[e];
           }
         }
       }
     }
-    if (c >= nch) continue;
-    const bool cached = kind == 2 || (kind == 1 && a.slots);
+    if (head[i] < 0) continue;
+    const bool cached = kind[i] == 2 || (kind[i] == 1 && a.slots);
+    if (cached && !keep) continue;
+    const HeadView& d = !cached ? (kind[i] == 0 ? a.q_out : a.k_out) : kind[i] == 1 ? a.kc : a.vc;
+    const int64_t at = (cached ? page * d.ps + in * d.ts : t * d.ts) + head[i] * d.hs + c * 8;
     if (!cached || !a.cache8) {
-      uint16_t* out;
-      if (cached) {
-        if (!keep) continue;
-        const HeadView& d = kind == 1 ? a.kc : a.vc;
-        out = (uint16_t*)d.p + page * d.ps + h * d.hs + in * d.ts + c * 8;
-      } else {
-        const HeadView& d = kind == 0 ? a.q_out : a.k_out;
-        out = (uint16_t*)d.p + t * d.ts + h * d.hs + c * 8;
-      }
       i32x4 w;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w[i] = (int)((uint32_t)f32_to_h<F16>(y[2 * i]) | ((uint32_t)f32_to_h<F16>(y[2 * i + 1]) << 16));
-      *(i32x4*)out = w;
+      for (int e = 0; e < 4; ++e) w[e] = pack2<F16>(y[2 * e], y[2 * e + 1]);
+      *(i32x4*)((uint16_t*)d.p + at) = w;
     } else {
-      if (!keep) continue;
-      const HeadView& d = kind == 1 ? a.kc : a.vc;
-      const float* sp = kind == 1 ? a.k_scale : a.v_scale;
-      const float s = sp ? sp[h] : 1.f;
+      const float* sp = kind[i] == 1 ? a.k_scale : a.v_scale;
+      const float s = sp ? sp[head[i]] : 1.f;
       // Saturated to the type's range; a NaN passes the comparisons and
       // stays one.
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float z = y[i] / s;
-        y[i] = z > 448.f ? 448.f : z < -448.f ? -448.f : z;
+      for (int e = 0; e < 8; ++e) {
+        const float z = y[e] / s;
+        y[e] = z > 448.f ? 448.f : z < -448.f ? -448.f : z;
       }
       i32x2 w;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        int word = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i], y[4 * i + 1], 0, false);
-        w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * i + 2], y[4 * i + 3], word, true);
+      for (int e = 0; e < 2; ++e) {
+        int word = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * e], y[4 * e + 1], 0, false);
+        w[e] = __builtin_amdgcn_cvt_pk_fp8_f32(y[4 * e + 2], y[4 * e + 3], word, true);
       }
-      *(i32x2*)((uint8_t*)d.p + page * d.ps + h * d.hs + in * d.ts + c * 8) = w;
+      *(i32x2*)((uint8_t*)d.p + at) = w;
     }
   }
 }
 
-template <bool F16> hipError_t launch_heads_t(const HeadArgs& a, int64_t T, hipStream_t s) {
-  const int nch = a.D / 8;
-  const int lph = nch <= 2 ? 2 : nch <= 4 ? 4 : nch <= 8 ? 8 : nch <= 16 ? 16 : 32;
-  const int groups = RP_THREADS / lph;
-  const int heads = a.Hq + a.Hk + a.Hv;
-  const unsigned gy = (unsigned)((heads + groups - 1) / groups);
-  const dim3 grid((unsigned)T, gy);
-  switch (lph) {
-    case 2: hipLaunchKernelGGL((heads_kernel<F16, 2>), grid, dim3(RP_THREADS), 0, s, a); break;
-    case 4: hipLaunchKernelGGL((heads_kernel<F16, 4>), grid, dim3(RP_THREADS), 0, s, a); break;
-    case 8: hipLaunchKernelGGL((heads_kernel<F16, 8>), grid, dim3(RP_THREADS), 0, s, a); break;
-    case 16: hipLaunchKernelGGL((heads_kernel<F16, 16>), grid, dim3(RP_THREADS), 0, s, a); break;
-    default: hipLaunchKernelGGL((heads_kernel<F16, 32>), grid, dim3(RP_THREADS), 0, s, a); break;
+template <bool F16, int LPH> hipError_t launch_heads_l(const HeadArgs& a, int64_t T, hipStream_t s) {
+  constexpr int HPW = 64 / LPH;
+  const int jobs = (a.Hq + HPW - 1) / HPW + (a.Hk + HPW - 1) / HPW + (a.Hv + HPW - 1) / HPW;
+  const int blocks = (jobs + RP_WAVES - 1) / RP_WAVES;  // of one job per wave
+  // Few tokens: one job per wave, for the shortest chain.  Many: three.
+  if (T * blocks <= 2048 || blocks < 2) {
+    hipLaunchKernelGGL((heads_kernel<F16, LPH, 1>), dim3((unsigned)T, (unsigned)blocks),
+                       dim3(RP_THREADS), 0, s, a);
+  } else {
+    hipLaunchKernelGGL((heads_kernel<F16, LPH, 3>), dim3((unsigned)T, (unsigned)((blocks + 2) / 3)),
+                       dim3(RP_THREADS), 0, s, a);
   }
   return hipGetLastError();
+}
+
+template <bool F16> hipError_t launch_heads_t(const HeadArgs& a, int64_t T, hipStream_t s) {
+  const int nch = a.D / 8;
+  if (nch <= 2) return launch_heads_l<F16, 2>(a, T, s);
+  if (nch <= 4) return launch_heads_l<F16, 4>(a, T, s);
+  if (nch <= 8) return launch_heads_l<F16, 8>(a, T, s);
+  if (nch <= 16) return launch_heads_l<F16, 16>(a, T, s);
+  return launch_heads_l<F16, 32>(a, T, s);
 }
 
 }  // namespace

@@ -32,6 +32,8 @@ _SCORE = struct.Struct("<6qd5q")
 _DTYPE16 = {torch.bfloat16: 0, torch.float16: 1}
 _SCORE_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _NO = (0, 0, 0)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def declare(lib):
@@ -104,9 +106,11 @@ def _forward_only(*tensors):
 
 
 def _stream_of(stream, t):
+    # the current stream's address without the Stream object that
+    # torch.cuda.current_stream builds: 0.2 instead of 4 us of a 10 us call
     if stream is not None:
         return stream.cuda_stream
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return _raw_stream(t.get_device())
 
 
 class ServingOps:
