@@ -161,6 +161,25 @@ int ensure_bytes(lin_gemm_t h, size_t need, hipStream_t s) {
   return LIN_OK;
 }
 
+// The handle's arrival counters (at zero between calls) are at least n.
+int ensure_counters(lin_gemm_t h, size_t n, hipStream_t s) {
+  if (n <= h->counters_n) return LIN_OK;
+  hipError_t e = hipStreamSynchronize(s);  // in-flight calls may still use the old ones
+  if (e != hipSuccess) return hip_fail(h, e, "hipStreamSynchronize");
+  if (h->counters) h->retired.push_back(h->counters);
+  h->counters = nullptr;
+  h->counters_n = 0;
+  const size_t bytes = grow_size(n * sizeof(int));
+  if (hipMalloc(&h->counters, bytes) != hipSuccess) {
+    h->counters = nullptr;
+    return fail(h, LIN_ERR_OOM, "arrival counter allocation failed");
+  }
+  e = lg::launch_fill_zero(h->counters, bytes, s);
+  if (e != hipSuccess) return hip_fail(h, e, "counter zero fill");
+  h->counters_n = bytes / sizeof(int);
+  return LIN_OK;
+}
+
 int run_attention(lin_gemm_t h, const lin_attention_t* p, hipStream_t s) {
   if (!p) return fail(h, LIN_ERR_INVALID_ARG, "null arguments");
   if (p->dtype != LIN_Q_BF16 && p->dtype != LIN_Q_FP16)
@@ -303,6 +322,9 @@ int run_score(lin_gemm_t h, const lin_score_t* p, hipStream_t s) {
     if (rc != LIN_OK) return rc;
     a.part_keys = (uint64_t*)h->ws;
     a.part_sums = (float*)((char*)h->ws + keys);
+    rc = ensure_counters(h, (size_t)a.T * lg::SCORE_COUNTER_STEP, s);
+    if (rc != LIN_OK) return rc;
+    a.counters = h->counters;
   }
   hipError_t e = lg::launch_score(a, (int)p->dtype, s);
   return e == hipSuccess ? LIN_OK : hip_fail(h, e, "log-probability launch");

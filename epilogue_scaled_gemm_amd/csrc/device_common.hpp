@@ -127,6 +127,16 @@ __device__ inline float e8m0_to_f32(uint32_t e) { return __uint_as_float(e << 23
 __device__ inline i32x4 lo16(const i32x8& v) { return i32x4{v[0], v[1], v[2], v[3]}; }
 __device__ inline i32x4 hi16(const i32x8& v) { return i32x4{v[4], v[5], v[6], v[7]}; }
 
+// ------------------------------------------------- agent-scope accesses
+// Coherent across the XCDs' L2s by themselves (partials that another workgroup
+// reads in the same launch).
+template <typename T> __device__ inline T ld_agent(const T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <typename T> __device__ inline void st_agent(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // ---------------------------------------------------------- conversions
 __device__ inline float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
 __device__ inline float f16_bits_to_f32(uint32_t b) {

@@ -48,13 +48,6 @@ namespace {
 
 constexpr int STEPB = 128;  // bytes of K per step
 
-template <typename T> __device__ inline T ld_agent(const T* p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-template <typename T> __device__ inline void st_agent(T* p, T v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-
 // 16-byte load that is always issued (the address is valid whatever `ok`
 // says) and then zeroed when `ok` is false: straight-line code, so the
 // compiler knows how many loads are outstanding and can wait for one batch

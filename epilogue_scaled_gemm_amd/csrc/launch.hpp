@@ -206,11 +206,14 @@ struct ScoreArgs {
   float* top_logprobs;
   float* part_sums;        // [T][nsplit][3]
   uint64_t* part_keys;     // [T][nsplit][k]
+  int* counters;           // [T][SCORE_COUNTER_STEP] arrivals, zero between calls (nsplit > 1)
   int64_t T, V, stride, slice;
   int k, nsplit;
   float c, inv_t;          // log2(e) / temperature, 1 / temperature
 };
 constexpr int SCORE_MAX_TOP = 32;
+constexpr int SCORE_COUNTER_STEP = 32;  // a cache line per row's arrivals
+constexpr int SCORE_BATCHES = 64;  // of a wave in one slice, at most
 // elem: 0 bf16, 1 fp16, 2 fp32.
 void score_plan(int64_t T, int64_t V, int elem, int* nsplit, int64_t* slice);
 hipError_t launch_score(const ScoreArgs& a, int elem, hipStream_t s);
