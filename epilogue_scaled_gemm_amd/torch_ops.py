@@ -9,6 +9,9 @@
 - ``torch.ops.lingemm.scaled_linear_grouped``: the mixture-of-experts form
   (lin_gemm_run_grouped): token-sorted rows, one weight per expert; and
   ``scaled_linear_grouped_dynamic`` for 16-bit activations quantized first.
+- ``torch.ops.lingemm.qk_norm_rope``, ``kv_append``, ``tree_attention`` and
+  ``token_logprobs``: the serving operators between the layers (the handle's
+  methods of ``serving``), forward only.
 - ``fuse_linear_epilogues(gm, example_inputs)``: a torch.fx pass that
   rewrites ``linear -> activation [-> * alpha] [-> + residual]`` chains of a
   traced module, and the ``matmul(x, w) -> + bias -> activation ...`` chain
@@ -36,7 +39,7 @@ graph, run them once eagerly on the capture stream
 shape of the built-in table) capture on any stream.
 """
 import operator
-from typing import Optional
+from typing import Optional, Tuple
 
 import torch
 import torch.nn.functional as F
@@ -265,6 +268,122 @@ def _scaled_linear_grouped_dynamic_fake(x, weight, offsets, scale_b, bias=None, 
                                         quant="fp8_dynamic", act="none", alpha=1.0, max_rows=0):
     torch._check(offsets.shape[0] == weight.shape[0] + 1)
     return x.new_empty((x.shape[0], weight.shape[1]), dtype=torch.bfloat16)
+
+
+# ------------------------------------------------------- serving operators
+#
+# Outputs are allocated on the calling stream, as above; the checks are the
+# binding's.  Rows that no sequence owns are left as allocated.
+
+def _check_heads16(name, t):
+    if t.dim() != 3 or t.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{name} must be [tokens, heads, dim] in bfloat16 or float16")
+
+
+@torch.library.custom_op("lingemm::qk_norm_rope", mutates_args=())
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos_sin: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 interleaved: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Per-head norms (where weights are given) and the position rotation
+    (where a table is) of q [T, Hq, dim] and k [T, Hk, dim]; new tensors."""
+    _check_heads16("q", q)
+    _check_heads16("k", k)
+    return handle_for(q.device).qk_norm_rope(
+        q, k, torch.empty(q.shape, dtype=q.dtype, device=q.device),
+        torch.empty(k.shape, dtype=k.dtype, device=k.device), cos_sin=cos_sin, positions=positions,
+        q_weight=q_weight, k_weight=k_weight, eps=eps, interleaved=interleaved)
+
+
+@qk_norm_rope.register_fake
+def _qk_norm_rope_fake(q, k, cos_sin=None, positions=None, q_weight=None, k_weight=None, eps=1e-6,
+                       interleaved=False):
+    _check_heads16("q", q)
+    _check_heads16("k", k)
+    return q.new_empty(q.shape), k.new_empty(k.shape)
+
+
+@torch.library.custom_op("lingemm::kv_append", mutates_args=("k_cache", "v_cache"))
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              slots: torch.Tensor, cos_sin: Optional[torch.Tensor] = None,
+              positions: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+              eps: float = 1e-6, interleaved: bool = False, k_scale: Optional[torch.Tensor] = None,
+              v_scale: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+              q_weight: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Store k and v at slots of the paged caches (in place), the keys
+    normalised and rotated on the way.  Returns q normalised and rotated by
+    the same launch (an empty tensor without one)."""
+    _check_heads16("k", k)
+    if q is None:
+        q_out = None
+    else:
+        _check_heads16("q", q)
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    handle_for(k.device).kv_append(k, v, k_cache, v_cache, slots, cos_sin=cos_sin,
+                                   positions=positions, k_weight=k_weight, eps=eps,
+                                   interleaved=interleaved, k_scale=k_scale, v_scale=v_scale, q=q,
+                                   q_out=q_out, q_weight=q_weight)
+    return k.new_empty(0) if q_out is None else q_out
+
+
+@kv_append.register_fake
+def _kv_append_fake(k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, k_weight=None,
+                    eps=1e-6, interleaved=False, k_scale=None, v_scale=None, q=None, q_weight=None):
+    _check_heads16("k", k)
+    return k.new_empty(0) if q is None else q.new_empty(q.shape)
+
+
+@torch.library.custom_op("lingemm::tree_attention", mutates_args=())
+def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   page_table: torch.Tensor, context: torch.Tensor, offsets: torch.Tensor,
+                   max_context: int, max_nodes: int, mask: Optional[torch.Tensor] = None,
+                   scale: Optional[float] = None, k_scale: Optional[torch.Tensor] = None,
+                   v_scale: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention of the nodes q [T, Hq, dim] over their sequences' paged
+    caches; returns (out [T, Hq, dim], lse [T, Hq] fp32)."""
+    _check_heads16("q", q)
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    handle_for(q.device).tree_attention(q, k_cache, v_cache, out, page_table, context, offsets,
+                                        max_context=max_context, max_nodes=max_nodes, mask=mask,
+                                        scale=scale, k_scale=k_scale, v_scale=v_scale, lse=lse)
+    return out, lse
+
+
+@tree_attention.register_fake
+def _tree_attention_fake(q, k_cache, v_cache, page_table, context, offsets, max_context, max_nodes,
+                         mask=None, scale=None, k_scale=None, v_scale=None):
+    _check_heads16("q", q)
+    return q.new_empty(q.shape), q.new_empty(q.shape[:2], dtype=torch.float32)
+
+
+@torch.library.custom_op("lingemm::token_logprobs", mutates_args=())
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0,
+                   temperature: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor,
+                                                      torch.Tensor]:
+    """(log probabilities [T] of tokens, entropies [T], the top tokens' ids
+    int32 [T, top] and log probabilities [T, top]) under logits [T, V]."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab]")
+    T, dev = logits.shape[0], logits.device
+    logprobs = torch.empty(T, dtype=torch.float32, device=dev)
+    entropy = torch.empty(T, dtype=torch.float32, device=dev)
+    ids = torch.empty(T, top, dtype=torch.int32, device=dev)
+    best = torch.empty(T, top, dtype=torch.float32, device=dev)
+    handle_for(dev).token_logprobs(logits, tokens, logprobs, entropy=entropy,
+                                   top_ids=ids if top else None, top_logprobs=best if top else None,
+                                   temperature=temperature)
+    return logprobs, entropy, ids, best
+
+
+@token_logprobs.register_fake
+def _token_logprobs_fake(logits, tokens, top=0, temperature=1.0):
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocab]")
+    T = logits.shape[0]
+    f32 = dict(dtype=torch.float32)
+    return (logits.new_empty(T, **f32), logits.new_empty(T, **f32),
+            logits.new_empty((T, top), dtype=torch.int32), logits.new_empty((T, top), **f32))
 
 
 # --------------------------------------------------------------- FX rewrite
