@@ -275,6 +275,11 @@ int run_attention(lin_gemm_t h, const lin_attention_t* p, hipStream_t s) {
     if (rc != LIN_OK) return rc;
     a.part_o = (float*)h->ws;
     a.part_ml = a.part_o + n * (size_t)p->dim;
+    if (plan.arrival) {
+      rc = ensure_counters(h, (size_t)(p->sequences * a.Hk) * (size_t)a.ntiles * lg::AT_COUNTER_STEP, s);
+      if (rc != LIN_OK) return rc;
+      a.counters = h->counters;
+    }
   }
   hipError_t e = lg::launch_attention(a, (int)p->dim, plan.shape, p->dtype == LIN_Q_FP16, kv8, s);
   return e == hipSuccess ? LIN_OK : hip_fail(h, e, "attention launch");

@@ -26,8 +26,8 @@
 //  - tile_kernel (many rows: large trees, parts of prompts; bound by the
 //    matrix units): 32 rows per wave, all waves share each tile of
 //    positions in LDS, double-buffered.
-// Long contexts are split over workgroups; those write (m, l, O) in 32 bits
-// and join_kernel joins them.
+// Long contexts are split over workgroups; those write (m, l, O) in 32 bits,
+// and join_kernel, or of few workgroups the last to arrive, joins them.
 #include <type_traits>
 
 #include "launch.hpp"
@@ -272,7 +272,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
     const int row0 = tile * 16 * NQ;
     const int last = min(row0 + 16 * NQ - 1, nrows - 1) / a.G;
     int lo, hi;
-    const int nsp = split_range(a, j, last, lo, hi);
+    int nsp = split_range(a, j, last, lo, hi);
+    if (tile >= a.ntiles && a.counters) {
+      // more nodes than the call's bound: there is no arrival counter, and
+      // the first split takes the whole row tile
+      lo = 0;
+      hi = a.mask ? j.len : min(j.len, j.ctx + last + 1);
+      nsp = 1;
+    }
     if (j.split >= nsp) continue;
     const int nblk = (hi - lo + 31) / 32;
 
@@ -508,13 +515,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
       }
       __syncthreads();
     }
+    const int heads = a.Hk * a.G;
+    auto row_of = [&](int row) {  // of q and out
+      return (int64_t)(j.t0 + row / a.G) * heads + j.hk * a.G + row % a.G;
+    };
+    const float vscale = a.v_scale ? a.v_scale[j.hk] : 1.f;
     if (wave == 0) {
-      const float vscale = a.v_scale ? a.v_scale[j.hk] : 1.f;
 #pragma unroll
       for (int q = 0; q < NQ; ++q) {
         if (!live[q]) continue;
-        const int row = row0 + q * 16 + col;
-        const int64_t r = (int64_t)(j.t0 + node[q]) * (a.Hk * a.G) + j.hk * a.G + row % a.G;
+        const int64_t r = row_of(row0 + q * 16 + col);
         if (nsp == 1) {
           const float inv = inverse_sum(l[q], vscale);
 #pragma unroll
@@ -525,12 +535,76 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
           if (a.lse && grp == 0) a.lse[r] = row_lse(m[q], l[q]);
         } else {
           const int64_t pr = (int64_t)j.split * a.rows + r;
+          if (!a.counters) {
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt) *(f32x4*)(a.part_o + pr * D + dt * 16 + grp * 4) = o[q][dt];
-          if (grp == 0) *(float2*)(a.part_ml + pr * 2) = make_float2(m[q], l[q]);
+            for (int dt = 0; dt < DT; ++dt)
+              *(f32x4*)(a.part_o + pr * D + dt * 16 + grp * 4) = o[q][dt];
+            if (grp == 0) *(float2*)(a.part_ml + pr * 2) = make_float2(m[q], l[q]);
+            continue;
+          }
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2)
+              st_agent((double*)(a.part_o + pr * D + dt * 16 + grp * 4 + i),
+                       __builtin_bit_cast(double, make_float2(o[q][dt][i], o[q][dt][i + 1])));
+          if (grp == 0)
+            st_agent((double*)(a.part_ml + pr * 2), __builtin_bit_cast(double, make_float2(m[q], l[q])));
         }
       }
     }
+    if (nsp == 1 || !a.counters) {
+      __syncthreads();  // smem is written again for the next row tile
+      continue;
+    }
+    // Arrival: the workgroup that comes last joins the splits.  Partials are
+    // written and read with agent-scope atomics, which are coherent across the
+    // XCDs' L2s by themselves; the wave waits for its stores to be
+    // acknowledged before it counts itself.  (A release / acquire of that
+    // scope would write back and invalidate the whole L2 every time.)
+    int* const counter = a.counters + ((int64_t)(j.b * a.Hk + j.hk) * a.ntiles + tile) * AT_COUNTER_STEP;
+    int* const arrival = (int*)st;
+    if (wave == 0) {
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      __builtin_amdgcn_s_waitcnt(0);
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+      if (lane == 0)
+        *arrival = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    const bool is_last = *arrival == nsp - 1;
+    __syncthreads();  // smem is written again for the next row tile
+    if (!is_last) continue;
+    constexpr int LPR = D / 4;  // lanes of a row
+    const int c4 = threadIdx.x % LPR * 4;
+    for (int row = row0 + threadIdx.x / LPR; row < min(row0 + 16 * NQ, nrows); row += 256 / LPR) {
+      const int64_t r = row_of(row);
+      auto pair = [](const float* p) {
+        return __builtin_bit_cast(float2, ld_agent((const double*)p));
+      };
+      float M = NEG_INF;
+      for (int i = 0; i < nsp; ++i) M = fmaxf(M, pair(a.part_ml + (i * a.rows + r) * 2).x);
+      const float ms = M == NEG_INF ? 0.f : M;
+      float L = 0.f;
+      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (int i = 0; i < nsp; ++i) {
+        const int64_t pr = i * a.rows + r;
+        const float2 ml = pair(a.part_ml + pr * 2);
+        const float2 x = pair(a.part_o + pr * D + c4), y = pair(a.part_o + pr * D + c4 + 2);
+        const float f = exp2_fast(ml.x - ms);
+        L += f * ml.y;
+        acc[0] += f * x.x;
+        acc[1] += f * x.y;
+        acc[2] += f * y.x;
+        acc[3] += f * y.y;
+      }
+      const float inv = inverse_sum(L, vscale);
+      *(i32x2*)(a.out + r * D + c4) =
+          i32x2{pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv)};
+      if (a.lse && c4 == 0) a.lse[r] = row_lse(M, L);
+    }
+    if (threadIdx.x == 0) st_agent(counter, 0);  // kept at zero between calls
   }
 }
 
@@ -709,9 +783,10 @@ __device__ inline int again(int x) {
   return x;
 }
 
-// A barrier that waits for nothing but the other waves.
-__device__ inline void phase_barrier() {
+// A barrier that waits for the wave's LDS accesses, but for none of its loads.
+__device__ inline void tile_barrier() {
   asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -726,17 +801,24 @@ template <int D> constexpr int tile_lds_bytes() { return TILE_BUFS * tile_positi
 // CW = 2: 128 rows, waves 4..7 take the second half of each tile's positions
 // and their sums are joined at the end.
 //
-// The two waves of a SIMD alternate: while one runs the products of a block
-// (values of this one, keys of the next) the other runs its softmax, in
-// phases between barriers, waves 4..7 one phase behind waves 0..3.  With NB
-// blocks per wave and tile, wave group g has the softmax of block k of tile
-// it in phase 2 NB it + 2 k + g and its products in the next.  So
-//  - tile it - 1 is last read in phase 2 NB it, and its buffer is refilled
-//    (with tile it + 3) from the next phase on;
-//  - tile it + 1 is first read in phase 2 NB it + 2 NB - 1: every wave has
-//    waited for its own loads of it by the end of the phase before.
-// 16-bit caches go from memory to LDS directly, three tiles ahead; 8-bit
-// codes pass through registers, where they are widened.
+// One barrier per tile: past the one that ends step it, every wave has read
+// tile it to the end (its buffer may be refilled) and waited for its own
+// loads of tile it + 1 (which may be read).  16-bit caches go from memory to
+// LDS directly, issued three tiles ahead; 8-bit codes pass through registers
+// one tile ahead, where they are widened.  Waves 4..7 have the higher issue
+// priority, which keeps the two waves of a SIMD out of step: one's products
+// run under the other's exponentials.
+//
+// Bound by issue: a wave needs about 400 instructions per tile for its 32
+// MFMAs, and two waves per SIMD (what 250 registers allow) do not hide each
+// other fully.  Four trees of 64 nodes with four heads to a key head over
+// 32000 positions (dim 128, bf16): 175 us in this kernel, of which the tiles'
+// way into LDS alone takes 103 (5.1 TB/s) and the arithmetic alone 143 (0.94
+// PFLOP/s); 1500 nodes over 5001: 0.86 PFLOP/s.  Measured and not kept:
+// strict alternation of the two waves between barriers (215 us), the first
+// product of the next block inside the softmax of this one (spills), fragments
+// of the values read before the softmax (spills), page numbers by scalar loads
+// (their counter is the LDS reads' too: 195 us).
 template <int D, int CW, bool F16, bool KV8>
 __global__ __launch_bounds__(512) void tile_kernel(AttnArgs a) {
   constexpr int BM = 256 / CW, BN = tile_positions<D>();
@@ -816,8 +898,8 @@ __global__ __launch_bounds__(512) void tile_kernel(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int r = chunk_row(i, ln), c = ln % CPR;
-        const uint32_t page = min(max(g.p[i], 0), a.pages - 1);
         const int in = min(lo + it * BN + r, hi - 1) & a.page_mask;
+        const uint32_t page = min(max(g.p[i], 0), a.pages - 1);
         const char* ka = kb + (uint64_t)page * k_ps + in * k_ts;
         const char* va = vb + (uint64_t)page * v_ps + in * v_ts;
         if constexpr (KV8) {
@@ -909,7 +991,7 @@ __global__ __launch_bounds__(512) void tile_kernel(AttnArgs a) {
         }
       }
       finish(it + 1, 2);
-      phase_barrier();
+      tile_barrier();
       // (past the last block: of whatever the next buffer holds, not used)
       if (busy) w.scores(p, buffer(it + 1), b0 * 32, lane);
     };
@@ -1137,7 +1219,7 @@ hipError_t launch_one(const AttnArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((tile_kernel<D, CW, F16, KV8>), dim3((unsigned)grid), dim3(512), lds, s, a);
   }
   e = hipGetLastError();
-  if (e != hipSuccess || a.nsplit == 1) return e;
+  if (e != hipSuccess || a.nsplit == 1 || a.counters) return e;
   const int bm = attn_rows(SHAPE), rpb = 256 / (D / 4);
   const int64_t groups = std::min<int64_t>(((int64_t)a.ntiles * bm + rpb - 1) / rpb, 65535);
   hipLaunchKernelGGL((join_kernel<D, F16>),
@@ -1181,7 +1263,7 @@ AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t m
     // a few rounds of the 512 workgroups that run at a time, so that uneven
     // lengths even out
     ns = (1536 + units - 1) / units;
-    ns = std::min(ns, (steps + 1) / 2);
+    ns = std::min(ns, steps);
   } else {
     // as many as fill whole rounds best; splits of four tiles at least
     const int64_t slots = 256;
@@ -1196,6 +1278,10 @@ AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t m
   ns = std::max<int64_t>(1, ns);
   p.chunk = (steps + ns - 1) / ns * step;
   p.nsplit = std::max<int64_t>(1, (max_len + p.chunk - 1) / p.chunk);
+  // Joined by the last workgroup, a call of one token over 1024 positions
+  // takes 12 instead of 14.6 us; of 1536 workgroups the arrivals and the
+  // narrower stores cost 9 us where the second launch costs 5.6.
+  p.arrival = p.shape <= AT_STREAM32 && units * p.nsplit <= 512;
   return p;
 }
 

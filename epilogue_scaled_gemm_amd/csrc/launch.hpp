@@ -178,6 +178,8 @@ struct AttnArgs {
   const float *k_scale, *v_scale;
   float* part_o;           // [nsplit][rows][D]
   float* part_ml;          // [nsplit][rows][2]
+  int* counters;           // [sequences][Hk][ntiles][AT_COUNTER_STEP] arrivals, zero between
+                           // calls; null: join_kernel joins the splits
   int64_t q_ts, q_hs, k_ps, k_hs, k_ts, v_ps, v_hs, v_ts;
   int64_t T, rows, table_stride;
   int Hk, G, mask_words, max_pages, pages, page_log, page_mask;
@@ -186,12 +188,14 @@ struct AttnArgs {
 };
 // How a call is cut: the kernel and its row tile, ntiles workgroups over a
 // sequence's rows, nsplit splits of `chunk` positions.
+constexpr int AT_COUNTER_STEP = 16;  // ints; neighbours in lines of their own
 enum AttnShape : int { AT_STREAM16 = 0, AT_STREAM32 = 1, AT_TILE128 = 2, AT_TILE256 = 3 };
 inline constexpr int attn_rows(int shape) {
   return shape == AT_STREAM16 ? 16 : shape == AT_STREAM32 ? 32 : shape == AT_TILE128 ? 128 : 256;
 }
 struct AttnPlan {
   int shape;
+  bool arrival;  // the last workgroup joins the splits (else a second launch)
   int64_t ntiles, nsplit, chunk;
 };
 AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len);
