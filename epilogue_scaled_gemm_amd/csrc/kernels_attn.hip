@@ -23,9 +23,9 @@
 //    the cache): every wave runs through positions of its own, 32 at a time,
 //    without barriers: keys go from memory straight into MFMA operands,
 //    values through the wave's own LDS.
-//  - tile_kernel (many rows: large trees, parts of prompts; bound by the
-//    matrix units): 32 rows per wave, all waves share each tile of
-//    positions in LDS, double-buffered.
+//  - tile_kernel (many rows: large trees, parts of prompts; bound by issue
+//    and the matrix units): 32 rows per wave, all waves share each tile of
+//    positions in LDS, loaded up to three tiles ahead.
 // Long contexts are split over workgroups; those write (m, l, O) in 32 bits,
 // and join_kernel, or of few workgroups the last to arrive, joins them.
 #include <type_traits>
@@ -158,6 +158,13 @@ struct Job {
   bool flip, none;  // the sign of the scale goes to q; a zero scale: q is 0
 };
 
+// What lies beyond the page table (at most 2^30 positions) is cut off.
+__device__ inline void set_lengths(const AttnArgs& a, Job& j) {
+  const int most = a.max_pages << a.page_log;
+  j.ctx = min(max(a.context[j.b], 0), most);
+  j.len = min(j.ctx + j.n, most);
+}
+
 // Workgroup -> job.  Workgroups go to the eight XCDs in turn; the row tiles
 // that share keys follow each other on one XCD and find them in its L2.  A
 // malformed plan gives wrong rows, never an access outside the buffers.
@@ -174,8 +181,7 @@ __device__ inline bool find_job(const AttnArgs& a, Job& j) {
   const int64_t t1 = a.offsets[j.b + 1];
   if (j.t0 < 0 || t1 <= j.t0 || t1 > a.T) return false;
   j.n = (int)(t1 - j.t0);
-  j.ctx = max(a.context[j.b], 0);
-  j.len = (int)min((int64_t)j.ctx + j.n, (int64_t)a.max_pages << a.page_log);
+  set_lengths(a, j);
   const float sc = a.scale_log2e * (a.k_scale ? a.k_scale[j.hk] : 1.f);
   j.flip = sc < 0.f;
   j.none = sc == 0.f;
@@ -229,18 +235,129 @@ __device__ inline float row_lse(float m, float l) {
   return (m + __builtin_amdgcn_logf(l)) * 0.69314718056f;
 }
 
+// ------------------------------------------------------ joining the splits
+struct Part {
+  f32x4 o;  // four values of a row, not divided by l
+  float m, l;
+};
+__device__ inline void join(Part& x, const Part& y) {
+  const float m = fmaxf(x.m, y.m), ms = m == NEG_INF ? 0.f : m;
+  const float fx = exp2_fast(x.m - ms), fy = exp2_fast(y.m - ms);
+  x.m = m;
+  x.l = x.l * fx + y.l * fy;
+  x.o = x.o * fx + y.o * fy;
+}
+
+// A workgroup joins rows: D / 4 lanes hold one, `per` such groups take its
+// splits in turn with eight on their way, and the groups' sums meet in LDS.
+// `r` and `nsp` are the row of this thread and its splits (0: no row).  What
+// other workgroups of the same launch wrote is read with agent-scope loads.
+template <int D, bool F16, bool SAME_LAUNCH>
+__device__ ALWAYS_INLINE void join_rows(const AttnArgs& a, int64_t r, int nsp, int per, float vscale,
+                                        Part* parts) {
+  constexpr int LPR = D / 4;
+  const int c4 = threadIdx.x % LPR * 4, g = threadIdx.x / LPR % per;
+  auto pair = [](const float* q) {
+    if constexpr (SAME_LAUNCH) return __builtin_bit_cast(float2, ld_agent((const double*)q));
+    else return *(const float2*)q;
+  };
+  Part x = {{0.f, 0.f, 0.f, 0.f}, NEG_INF, 0.f};
+#pragma unroll 1
+  for (int i0 = g; i0 < nsp; i0 += 8 * per) {
+    float2 ml[8], u[8], v[8];
+    float m = x.m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      ml[i] = make_float2(NEG_INF, 0.f);
+      if (i0 + i * per >= nsp) continue;
+      const int64_t pr = (int64_t)(i0 + i * per) * a.rows + r;
+      ml[i] = pair(a.part_ml + pr * 2);
+      u[i] = pair(a.part_o + pr * D + c4);
+      v[i] = pair(a.part_o + pr * D + c4 + 2);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, ml[i].x);
+    const float ms = m == NEG_INF ? 0.f : m;
+    const float f0 = exp2_fast(x.m - ms);
+    x.m = m;
+    x.l *= f0;
+    x.o *= f0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i0 + i * per >= nsp) continue;
+      const float f = exp2_fast(ml[i].x - ms);
+      x.l += f * ml[i].y;
+      x.o[0] += f * u[i].x;
+      x.o[1] += f * u[i].y;
+      x.o[2] += f * v[i].x;
+      x.o[3] += f * v[i].y;
+    }
+  }
+  if (per > 1) {
+    parts[threadIdx.x] = x;
+    __syncthreads();
+    if (g == 0)
+      for (int i = 1; i < per; ++i) join(x, parts[threadIdx.x + i * LPR]);
+    __syncthreads();
+  }
+  if (g > 0 || nsp == 0) return;
+  const float inv = inverse_sum(x.l, vscale);
+  *(i32x2*)(a.out + r * D + c4) =
+      i32x2{pack2<F16>(x.o[0] * inv, x.o[1] * inv), pack2<F16>(x.o[2] * inv, x.o[3] * inv)};
+  if (a.lse && c4 == 0) a.lse[r] = row_lse(x.m, x.l);
+}
+
+// After a launch whose splits were left apart: blockIdx.y the group of rows.
+template <int D, bool F16>
+__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int bm, int per) {
+  __shared__ Part parts[256];
+  const int rows = 256 / (D / 4) / per;  // of a workgroup
+  const int hk = blockIdx.x % a.Hk, b = blockIdx.x / a.Hk;
+  Job j;
+  j.t0 = a.offsets[b];
+  const int64_t t1 = a.offsets[b + 1];
+  if (j.t0 < 0 || t1 <= j.t0 || t1 > a.T) return;
+  j.n = (int)(t1 - j.t0);
+  j.b = b;
+  set_lengths(a, j);
+  j.split = 0;
+  const float vscale = a.v_scale ? a.v_scale[hk] : 1.f;
+  for (int r0 = blockIdx.y * rows; r0 < j.n * a.G; r0 += gridDim.y * rows) {
+    const int row = r0 + threadIdx.x / (D / 4) / per;
+    int nsp = 0;
+    int64_t r = 0;
+    if (row < j.n * a.G) {
+      int lo, hi;
+      nsp = split_range(a, j, min(row / bm * bm + bm - 1, j.n * a.G - 1) / a.G, lo, hi);
+      if (nsp == 1) nsp = 0;  // written by its workgroup
+      r = (int64_t)(j.t0 + row / a.G) * (a.Hk * a.G) + hk * a.G + row % a.G;
+    }
+    join_rows<D, F16, false>(a, r, nsp, per, vscale, parts);
+  }
+}
+
 // ------------------------------------------------------------ few rows
-// NQ tiles of 16 rows.  S^T tiles are 16x16 (MFMA 16x16x32): lane l holds row
+// One tile of 16 rows.  S^T tiles are 16x16 (MFMA 16x16x32): lane l holds row
 // l % 16 and positions 4 (l / 16) + 0..3 of each, so two tiles of a block of
 // 32 positions make the eight positions of one lane in the second product;
 // the transposing reads of V take the same eight.
+//
+// Bound by reading the cache: 48 sequences of up to 8191 positions, 8 key
+// heads of 128 values, four query heads each, in 8-bit codes take 127 us
+// (4.8 TB/s) and in bf16 223 us (5.5 TB/s; a large read reaches 5.4 to 5.9).
+// Four waves without a barrier keep loads of 32 KB each on their way; with a
+// shared tile of 128 rows, of which 16 are used, the 8-bit call takes 231 us,
+// 200 x 1000 positions 297 instead of 84.  Short calls are a chain of
+// latencies (page, keys, scores, values, join): 10 us for one token over 1024.
 template <int D, bool KV8> constexpr int stream_tile_bytes() { return 32 * D * (KV8 ? 1 : 2); }
-template <int D, int NQ, bool KV8> constexpr int stream_lds_bytes() {
-  // the waves' values; at the end two waves' sums, and all waves' m and l
-  return std::max(4 * stream_tile_bytes<D, KV8>(), 2 * NQ * 16 * D * 4) + 4 * NQ * 16 * 8;
+template <int D, bool KV8> constexpr int stream_lds_bytes() {
+  // the waves' values; at the end two waves' sums, or the parts of the splits;
+  // behind them all waves' m and l
+  return std::max({4 * stream_tile_bytes<D, KV8>(), 2 * 16 * D * 4, 256 * (int)sizeof(Part)}) +
+         4 * 16 * 8;
 }
 
-template <int D, int NQ, bool F16, bool KV8>
+template <int D, bool F16, bool KV8>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs a) {
   constexpr int ES = KV8 ? 1 : 2;
   constexpr int RB = D * ES;           // bytes of a cache row
@@ -257,7 +374,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int grp = lane >> 4, col = lane & 15;
   char* const sv = smem + wave * VT;
-  float* const st = (float*)(smem + stream_lds_bytes<D, NQ, KV8>() - 4 * NQ * 16 * 8);
+  float* const st = (float*)(smem + stream_lds_bytes<D, KV8>() - 4 * 16 * 8);
 
   Job j;
   if (!find_job(a, j)) return;
@@ -268,9 +385,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
   const uint32_t k_ps = a.k_ps * ES, k_ts = a.k_ts * ES, v_ps = a.v_ps * ES, v_ts = a.v_ts * ES;
   const int nrows = j.n * a.G;
 
-  for (int tile = j.tile0; tile * (16 * NQ) < nrows; tile += a.ntiles) {
-    const int row0 = tile * 16 * NQ;
-    const int last = min(row0 + 16 * NQ - 1, nrows - 1) / a.G;
+  for (int tile = j.tile0; tile * 16 < nrows; tile += a.ntiles) {
+    const int row0 = tile * 16;
+    const int last = min(row0 + 16 - 1, nrows - 1) / a.G;
     int lo, hi;
     int nsp = split_range(a, j, last, lo, hi);
     if (tile >= a.ntiles && a.counters) {
@@ -284,36 +401,26 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
     const int nblk = (hi - lo + 31) / 32;
 
     // this lane's rows, as operands of the first product
-    bool live[NQ];
-    int node[NQ];
-    i32x4 qf[NQ][KS];
-    const int64_t* mrow[NQ];
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      const int row = row0 + q * 16 + col;
-      live[q] = row < nrows;
-      node[q] = live[q] ? row / a.G : 0;
-      const int64_t t = j.t0 + node[q];
-      const int head = j.hk * a.G + (live[q] ? row % a.G : 0);
+    const bool live = row0 + col < nrows;
+    const int node = live ? (row0 + col) / a.G : 0;
+    const int64_t t = j.t0 + node;
+    const int64_t* const mrow = a.mask ? a.mask + t * a.mask_words : nullptr;
+    i32x4 qf[KS];
+    {
+      const int head = j.hk * a.G + (live ? (row0 + col) % a.G : 0);
       const uint16_t* qp = a.q + t * a.q_ts + head * a.q_hs;
-      mrow[q] = a.mask ? a.mask + t * a.mask_words : nullptr;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         // a lane's 16 bytes of codes are two steps' operands
         const int d = KV8 ? (ks >> 1) * 64 + grp * 16 + (ks & 1) * 8 : ks * 32 + grp * 8;
-        qf[q][ks] = scaled_q(*(const i32x4*)(qp + d), j.flip, j.none || !live[q]);
+        qf[ks] = scaled_q(*(const i32x4*)(qp + d), j.flip, j.none || !live);
       }
     }
 
-    float m[NQ], l[NQ];
-    f32x4 o[NQ][DT];
+    float m = NEG_INF, l = 0.f;
+    f32x4 o[DT];
 #pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      m[q] = NEG_INF;
-      l[q] = 0.f;
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt) o[q][dt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int dt = 0; dt < DT; ++dt) o[dt] = f32x4{0.f, 0.f, 0.f, 0.f};
 
     // Pages of a block's 32 positions, one per lane (twice).
     auto load_pages = [&](int blk) {
@@ -370,11 +477,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
         *(i32x4*)v_at(r, lane % CPR) = vr[i];
       }
       odd = __any(odd);
-      f32x4 s[NQ][2];
+      f32x4 s[2];
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) s[q][kt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        s[kt] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
           i32x4 kf;
@@ -382,52 +488,47 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
             kf = widen8<F16>(kr[kt][ks >> 1][2 * (ks & 1)], kr[kt][ks >> 1][2 * (ks & 1) + 1]);
           else
             kf = kr[kt][ks];
-#pragma unroll
-          for (int q = 0; q < NQ; ++q) s[q][kt] = mfma16<F16>(kf, qf[q][ks], s[q][kt]);
+          s[kt] = mfma16<F16>(kf, qf[ks], s[kt]);
         }
       }
       if (blk + 4 < nblk) {
         load_block(blk + 4, pg);
         if (blk + 8 < nblk) pg = load_pages(blk + 8);
       }
-      i32x4 pf[NQ];
+      if (tail) {
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        if (tail) {
+        for (int kt = 0; kt < 2; ++kt) {
+          const uint32_t vis = sees4(a, j, node, mrow, base + kt * 16 + grp * 4, hi);
 #pragma unroll
-          for (int kt = 0; kt < 2; ++kt) {
-            const uint32_t vis = sees4(a, j, node[q], mrow[q], base + kt * 16 + grp * 4, hi);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[q][kt][i] = (vis >> i) & 1 ? s[q][kt][i] : NEG_INF;
-          }
+          for (int i = 0; i < 4; ++i) s[kt][i] = (vis >> i) & 1 ? s[kt][i] : NEG_INF;
         }
-        float mx = s[q][0][0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[q][i >> 2][i & 3]);
-        const float mn = fmaxf(m[q], quad_max(mx));
-        if (__any((mn - m[q]) * j.sc > SLACK)) {
-          const float f = mn == NEG_INF ? 1.f : exp2_fast((m[q] - mn) * j.sc);
-          m[q] = mn;
-          l[q] *= f;
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[q][dt][i] *= f;
-        }
-        const float ms = m[q] == NEG_INF ? 0.f : m[q] * j.sc;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          s[q][i >> 2][i & 3] = exp2_fast(fmaf(s[q][i >> 2][i & 3], j.sc, -ms));
-          sum += s[q][i >> 2][i & 3];
-        }
-        l[q] += sum;
-        // rounded to the value type: the products are then exact in the MFMA
-        // and summed in 32 bits
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-          pf[q][w] = pack2<F16>(s[q][w >> 1][2 * (w & 1)], s[q][w >> 1][2 * (w & 1) + 1]);
       }
+      float mx = s[0][0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i >> 2][i & 3]);
+      const float mn = fmaxf(m, quad_max(mx));
+      if (__any((mn - m) * j.sc > SLACK)) {
+        const float f = mn == NEG_INF ? 1.f : exp2_fast((m - mn) * j.sc);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[dt][i] *= f;
+      }
+      const float ms = m == NEG_INF ? 0.f : m * j.sc;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s[i >> 2][i & 3] = exp2_fast(fmaf(s[i >> 2][i & 3], j.sc, -ms));
+        sum += s[i >> 2][i & 3];
+      }
+      l += sum;
+      // rounded to the value type: the products are then exact in the MFMA and
+      // summed in 32 bits
+      i32x4 pf;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) pf[w] = pack2<F16>(s[w >> 1][2 * (w & 1)], s[w >> 1][2 * (w & 1) + 1]);
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();  // the lanes' values are in LDS
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -452,66 +553,50 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
         i32x4 vf = value(dt);
         if (odd) {
 #pragma unroll 1
-          for (int kind = 0; kind < 3; ++kind)
+          for (int kind = 0; kind < 3; ++kind) {
+            const f32x4 x = mfma16<F16>(where_kind<F16>(vf, kind), pf, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-            for (int q = 0; q < NQ; ++q) {
-              const f32x4 t = mfma16<F16>(where_kind<F16>(vf, kind), pf[q], f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-              for (int i = 0; i < 4; ++i) o[q][dt][i] += t[i] > 0.f ? kind_value(kind) : 0.f;
-            }
+            for (int i = 0; i < 4; ++i) o[dt][i] += x[i] > 0.f ? kind_value(kind) : 0.f;
+          }
           vf = finite_part<F16>(vf);
         }
-#pragma unroll
-        for (int q = 0; q < NQ; ++q) o[q][dt] = mfma16<F16>(vf, pf[q], o[q][dt]);
+        o[dt] = mfma16<F16>(vf, pf, o[dt]);
       }
       __builtin_amdgcn_wave_barrier();  // read before the next block's are written
     }
 
     // Join the four waves.
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      l[q] = quad_sum(l[q]);
-      m[q] *= j.sc;
-      if (grp == 0) {
-        st[((wave * NQ + q) * 16 + col) * 2] = m[q];
-        st[((wave * NQ + q) * 16 + col) * 2 + 1] = l[q];
-      }
-    }
+    l = quad_sum(l);
+    m *= j.sc;
+    if (grp == 0) *(float2*)(st + (wave * 16 + col) * 2) = make_float2(m, l);
     __syncthreads();
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
+    {
       float M = NEG_INF, L = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) M = fmaxf(M, st[((w * NQ + q) * 16 + col) * 2]);
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, st[(w * 16 + col) * 2]);
       const float ms = M == NEG_INF ? 0.f : M;
 #pragma unroll
       for (int w = 0; w < 4; ++w)
-        L += st[((w * NQ + q) * 16 + col) * 2 + 1] *
-             exp2_fast(st[((w * NQ + q) * 16 + col) * 2] - ms);
-      const float f = exp2_fast(m[q] - ms);
+        L += st[(w * 16 + col) * 2 + 1] * exp2_fast(st[(w * 16 + col) * 2] - ms);
+      const float f = exp2_fast(m - ms);
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[q][dt][i] *= f;
-      m[q] = M;
-      l[q] = L;
+        for (int i = 0; i < 4; ++i) o[dt][i] *= f;
+      m = M;
+      l = L;
     }
     f32x4* const sums = (f32x4*)smem;
 #pragma unroll
     for (int step = 2; step > 0; step >>= 1) {
       if (wave >= step && wave < 2 * step) {
 #pragma unroll
-        for (int q = 0; q < NQ; ++q)
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-            sums[((wave - step) * NQ * DT + q * DT + dt) * 64 + lane] = o[q][dt];
+        for (int dt = 0; dt < DT; ++dt) sums[((wave - step) * DT + dt) * 64 + lane] = o[dt];
       }
       __syncthreads();
       if (wave < step) {
 #pragma unroll
-        for (int q = 0; q < NQ; ++q)
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt) o[q][dt] += sums[(wave * NQ * DT + q * DT + dt) * 64 + lane];
+        for (int dt = 0; dt < DT; ++dt) o[dt] += sums[(wave * DT + dt) * 64 + lane];
       }
       __syncthreads();
     }
@@ -520,43 +605,33 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
       return (int64_t)(j.t0 + row / a.G) * heads + j.hk * a.G + row % a.G;
     };
     const float vscale = a.v_scale ? a.v_scale[j.hk] : 1.f;
-    if (wave == 0) {
+    if (wave == 0 && live) {
+      const int64_t r = row_of(row0 + col);
+      const int64_t pr = (int64_t)j.split * a.rows + r;
+      if (nsp == 1) {
+        const float inv = inverse_sum(l, vscale);
 #pragma unroll
-      for (int q = 0; q < NQ; ++q) {
-        if (!live[q]) continue;
-        const int64_t r = row_of(row0 + q * 16 + col);
-        if (nsp == 1) {
-          const float inv = inverse_sum(l[q], vscale);
+        for (int dt = 0; dt < DT; ++dt)
+          *(i32x2*)(a.out + r * D + dt * 16 + grp * 4) =
+              i32x2{pack2<F16>(o[dt][0] * inv, o[dt][1] * inv),
+                    pack2<F16>(o[dt][2] * inv, o[dt][3] * inv)};
+        if (a.lse && grp == 0) a.lse[r] = row_lse(m, l);
+      } else if (!a.counters) {
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-            *(i32x2*)(a.out + r * D + dt * 16 + grp * 4) =
-                i32x2{pack2<F16>(o[q][dt][0] * inv, o[q][dt][1] * inv),
-                      pack2<F16>(o[q][dt][2] * inv, o[q][dt][3] * inv)};
-          if (a.lse && grp == 0) a.lse[r] = row_lse(m[q], l[q]);
-        } else {
-          const int64_t pr = (int64_t)j.split * a.rows + r;
-          if (!a.counters) {
+        for (int dt = 0; dt < DT; ++dt) *(f32x4*)(a.part_o + pr * D + dt * 16 + grp * 4) = o[dt];
+        if (grp == 0) *(float2*)(a.part_ml + pr * 2) = make_float2(m, l);
+      } else {
 #pragma unroll
-            for (int dt = 0; dt < DT; ++dt)
-              *(f32x4*)(a.part_o + pr * D + dt * 16 + grp * 4) = o[q][dt];
-            if (grp == 0) *(float2*)(a.part_ml + pr * 2) = make_float2(m[q], l[q]);
-            continue;
-          }
+        for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-            for (int i = 0; i < 4; i += 2)
-              st_agent((double*)(a.part_o + pr * D + dt * 16 + grp * 4 + i),
-                       __builtin_bit_cast(double, make_float2(o[q][dt][i], o[q][dt][i + 1])));
-          if (grp == 0)
-            st_agent((double*)(a.part_ml + pr * 2), __builtin_bit_cast(double, make_float2(m[q], l[q])));
-        }
+          for (int i = 0; i < 4; i += 2)
+            st_agent((double*)(a.part_o + pr * D + dt * 16 + grp * 4 + i),
+                     __builtin_bit_cast(double, make_float2(o[dt][i], o[dt][i + 1])));
+        if (grp == 0) st_agent((double*)(a.part_ml + pr * 2), __builtin_bit_cast(double, make_float2(m, l)));
       }
     }
-    if (nsp == 1 || !a.counters) {
-      __syncthreads();  // smem is written again for the next row tile
-      continue;
-    }
+    if (nsp == 1 || !a.counters) continue;  // (the last barrier is past smem's last use)
+
     // Arrival: the workgroup that comes last joins the splits.  Partials are
     // written and read with agent-scope atomics, which are coherent across the
     // XCDs' L2s by themselves; the wave waits for its stores to be
@@ -575,34 +650,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
     const bool is_last = *arrival == nsp - 1;
     __syncthreads();  // smem is written again for the next row tile
     if (!is_last) continue;
-    constexpr int LPR = D / 4;  // lanes of a row
-    const int c4 = threadIdx.x % LPR * 4;
-    for (int row = row0 + threadIdx.x / LPR; row < min(row0 + 16 * NQ, nrows); row += 256 / LPR) {
-      const int64_t r = row_of(row);
-      auto pair = [](const float* p) {
-        return __builtin_bit_cast(float2, ld_agent((const double*)p));
-      };
-      float M = NEG_INF;
-      for (int i = 0; i < nsp; ++i) M = fmaxf(M, pair(a.part_ml + (i * a.rows + r) * 2).x);
-      const float ms = M == NEG_INF ? 0.f : M;
-      float L = 0.f;
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-      for (int i = 0; i < nsp; ++i) {
-        const int64_t pr = i * a.rows + r;
-        const float2 ml = pair(a.part_ml + pr * 2);
-        const float2 x = pair(a.part_o + pr * D + c4), y = pair(a.part_o + pr * D + c4 + 2);
-        const float f = exp2_fast(ml.x - ms);
-        L += f * ml.y;
-        acc[0] += f * x.x;
-        acc[1] += f * x.y;
-        acc[2] += f * y.x;
-        acc[3] += f * y.y;
-      }
-      const float inv = inverse_sum(L, vscale);
-      *(i32x2*)(a.out + r * D + c4) =
-          i32x2{pack2<F16>(acc[0] * inv, acc[1] * inv), pack2<F16>(acc[2] * inv, acc[3] * inv)};
-      if (a.lse && c4 == 0) a.lse[r] = row_lse(M, L);
+    const int end = min(row0 + 16, nrows);
+    int per = 256 / (D / 4);  // groups of lanes per row
+    while (per > 1 && 256 / (D / 4) / per < end - row0) per >>= 1;
+    const int g = threadIdx.x / (D / 4);
+    for (int r0 = row0; r0 < end; r0 += 256 / (D / 4) / per) {
+      const int row = r0 + g / per;
+      join_rows<D, F16, true>(a, row < end ? row_of(row) : 0, row < end ? nsp : 0, per, vscale,
+                              (Part*)smem);
     }
     if (threadIdx.x == 0) st_agent(counter, 0);  // kept at zero between calls
   }
@@ -644,6 +699,13 @@ __device__ inline void clear(f32x16& p) {
   for (int i = 0; i < 16; ++i) p[i] = 0.f;
 }
 
+// x, as a value of its own: what is computed from it is not kept in registers
+// over a loop that has better use for them.
+__device__ inline int again(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // One wave's 32 rows: what the tile kernels keep of them.
 template <int D, bool F16> struct Rows {
   static constexpr int DT = D / 32, KS = D / 16;
@@ -655,6 +717,7 @@ template <int D, bool F16> struct Rows {
   // the products that use them.
   __device__ inline ALWAYS_INLINE void scores(f32x16& p, const char* sk, int r0, int lane) {
     constexpr int KA = 4;
+    if constexpr (D == 256) lane = again(lane);
     const int col = lane & 31, half = lane >> 5;
     i32x4 kf[KS];
     clear(p);
@@ -711,6 +774,7 @@ template <int D, bool F16> struct Rows {
   template <bool TAIL>
   __device__ inline ALWAYS_INLINE void values(const i32x4 (&pf)[2], const char* sv, int r0, int lane) {
     constexpr int NF = 2 * DT, VA = 4 < NF ? 4 : NF;
+    if constexpr (D == 256) lane = again(lane);
     if constexpr (TAIL) {
       bool odd = false;
 #pragma unroll
@@ -776,13 +840,6 @@ template <int D, bool F16> struct Rows {
 // s_waitcnt immediate for "vmcnt <= n" (other counters not waited for).
 constexpr int vmcnt_imm(int n) { return (n & 15) | 0x0F70 | ((n >> 4) << 14); }
 
-// x, as a value of its own: what is computed from it is not kept in registers
-// over a loop that has better use for them.
-__device__ inline int again(int x) {
-  asm volatile("" : "+v"(x));
-  return x;
-}
-
 // A barrier that waits for the wave's LDS accesses, but for none of its loads.
 __device__ inline void tile_barrier() {
   asm volatile("" ::: "memory");
@@ -794,6 +851,7 @@ __device__ inline void tile_barrier() {
 // Positions of a tile, and buffers of the tile kernel: 128 KB of LDS.
 template <int D> constexpr int tile_positions() { return 8192 / D; }
 constexpr int TILE_BUFS = 4;
+template <int D> constexpr int tile_waves() { return D == 256 ? 4 : 8; }
 template <int D> constexpr int tile_lds_bytes() { return TILE_BUFS * tile_positions<D>() * D * 4; }
 
 // Eight waves of 32 rows.  S^T tiles are 32x32 (MFMA 32x32x16): lane l holds
@@ -814,20 +872,26 @@ template <int D> constexpr int tile_lds_bytes() { return TILE_BUFS * tile_positi
 // other fully.  Four trees of 64 nodes with four heads to a key head over
 // 32000 positions (dim 128, bf16): 175 us in this kernel, of which the tiles'
 // way into LDS alone takes 103 (5.1 TB/s) and the arithmetic alone 143 (0.94
-// PFLOP/s); 1500 nodes over 5001: 0.86 PFLOP/s.  Measured and not kept:
+// PFLOP/s); 1500 nodes over 5001: 0.86 PFLOP/s.
+// Dim 256 has four waves, one per SIMD: O and Q of 32 rows take 200 registers.
+// 16 trees of 64 nodes over 2000 positions: 182 us (0.37 PFLOP/s: nothing runs
+// beside a wave's exponentials), and 208 with the LDS offsets of the fragments
+// kept over the loop, for which O went to memory.
+// Measured and not kept:
 // strict alternation of the two waves between barriers (215 us), the first
 // product of the next block inside the softmax of this one (spills), fragments
 // of the values read before the softmax (spills), page numbers by scalar loads
 // (their counter is the LDS reads' too: 195 us).
 template <int D, int CW, bool F16, bool KV8>
-__global__ __launch_bounds__(512) void tile_kernel(AttnArgs a) {
-  constexpr int BM = 256 / CW, BN = tile_positions<D>();
+__global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(AttnArgs a) {
+  constexpr int THREADS = 64 * tile_waves<D>();
+  constexpr int BM = THREADS / 2 / CW, BN = tile_positions<D>();
   constexpr int NB = BN / 32 / CW;
   constexpr int ES = KV8 ? 1 : 2;
   constexpr int CPR = D * ES / 16;       // 16-byte chunks of a cache row
-  constexpr int NI = BN * CPR / 512;     // chunks per thread, tile and operand
+  constexpr int NI = BN * CPR / THREADS; // chunks per thread, tile and operand
   constexpr int TILE = BN * D * 2;       // bytes of one operand's tile
-  static_assert(NI * 512 == BN * CPR, "whole chunks per thread");
+  static_assert(NI * THREADS == BN * CPR, "whole chunks per thread");
 
   extern __shared__ __align__(16) char smem[];  // [TILE_BUFS][keys, values]
   const int tid = threadIdx.x, lane = tid & 63;
@@ -1039,191 +1103,33 @@ __global__ __launch_bounds__(512) void tile_kernel(AttnArgs a) {
   }
 }
 
-// dim 256: O and Q of 32 rows take most of the registers of one wave per SIMD.
-// Four waves, tiles of 32 positions through registers into two buffers.
-template <bool F16, bool KV8>
-__global__ __launch_bounds__(256) void wide_kernel(AttnArgs a) {
-  constexpr int D = 256, BM = 128, BN = 32;
-  constexpr int ES = KV8 ? 1 : 2;
-  constexpr int CPR = D * ES / 16, NI = BN * CPR / 256, TILE = BN * D * 2;
-
-  extern __shared__ __align__(16) char smem[];  // [2][keys, values]
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int half = lane >> 5, col = lane & 31;
-
-  Job j;
-  if (!find_job(a, j)) return;
-  const int* const table = a.table + (int64_t)j.b * a.table_stride;
-  const char* const kb = (const char*)a.k + j.hk * a.k_hs * ES;
-  const char* const vb = (const char*)a.v + j.hk * a.v_hs * ES;
-  const uint32_t k_ps = a.k_ps * ES, k_ts = a.k_ts * ES, v_ps = a.v_ps * ES, v_ts = a.v_ts * ES;
-  const int nrows = j.n * a.G;
-
-  for (int tile = j.tile0; tile * BM < nrows; tile += a.ntiles) {
-    const int row0 = tile * BM;
-    const int last = min(row0 + BM - 1, nrows - 1) / a.G;
-    int lo, hi;
-    const int nsp = split_range(a, j, last, lo, hi);
-    if (j.split >= nsp) continue;
-    const int ntl = (hi - lo + BN - 1) / BN;
-    const int all = min(a.mask ? j.ctx : j.ctx + row0 / a.G + 1, hi);
-    const int full = max(0, (all - lo) / BN);
-
-    const int row = row0 + wave * 32 + col;
-    const bool live = row < nrows;
-    const int node = live ? row / a.G : 0;
-    const int64_t t = j.t0 + node;
-    const int head = j.hk * a.G + (live ? row % a.G : 0);
-    const int64_t* const mrow = a.mask ? a.mask + t * a.mask_words : nullptr;
-    Rows<D, F16> w;
-    {
-      const uint16_t* qp = a.q + t * a.q_ts + head * a.q_hs + half * 8;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
-        w.q[ks] = scaled_q(*(const i32x4*)(qp + ks * 16), j.flip, j.none || !live);
-    }
-    w.m = NEG_INF;
-    w.l = 0.f;
-#pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt) clear(w.o[dt]);
-
-    int pg[NI];
-    i32x4 rk[NI], rv[NI];
-    auto load_pages = [&](int it) ALWAYS_INLINE {
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-        pg[i] = table[min(lo + it * BN + (tid + i * 256) / CPR, hi - 1) >> a.page_log];
-    };
-    auto load_tile = [&](int it) ALWAYS_INLINE {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int r = (tid + i * 256) / CPR, c = tid % CPR;
-        const uint32_t page = min(max(pg[i], 0), a.pages - 1);
-        const int in = min(lo + it * BN + r, hi - 1) & a.page_mask;
-        rk[i] = *(const i32x4*)(kb + (uint64_t)page * k_ps + (in * k_ts + c * 16));
-        rv[i] = *(const i32x4*)(vb + (uint64_t)page * v_ps + (in * v_ts + c * 16));
-      }
-    };
-    auto store_tile = [&](int it) ALWAYS_INLINE {
-      char* const sk = smem + (it & 1) * 2 * TILE;
-      char* const sv = sk + TILE;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int r = (tid + i * 256) / CPR, c = tid % CPR;
-        if constexpr (KV8) {
-          *(i32x4*)(sk + k_off<D>(r, 2 * c)) = widen8<F16>(rk[i][0], rk[i][1]);
-          *(i32x4*)(sk + k_off<D>(r, 2 * c + 1)) = widen8<F16>(rk[i][2], rk[i][3]);
-          *(i32x4*)(sv + v_off<D>(r, 2 * c)) = widen8<F16>(rv[i][0], rv[i][1]);
-          *(i32x4*)(sv + v_off<D>(r, 2 * c + 1)) = widen8<F16>(rv[i][2], rv[i][3]);
-        } else {
-          *(i32x4*)(sk + k_off<D>(r, c)) = rk[i];
-          *(i32x4*)(sv + v_off<D>(r, c)) = rv[i];
-        }
-      }
-      __syncthreads();
-    };
-    load_pages(0);
-    load_tile(0);
-    if (ntl > 1) load_pages(1);
-    store_tile(0);
-    auto step = [&](int it, auto tail_tag) ALWAYS_INLINE {
-      constexpr bool TAIL = decltype(tail_tag)::value;
-      const char* const sk = smem + (it & 1) * 2 * TILE;
-      if (it + 1 < ntl) {
-        load_tile(it + 1);
-        if (it + 2 < ntl) load_pages(it + 2);
-      }
-      f32x16 p;
-      i32x4 pf[2];
-      w.scores(p, sk, 0, lane);
-      w.template softmax<TAIL>(p, pf, a, j, node, mrow, lo + it * BN, hi, lane);
-      w.template values<TAIL>(pf, sk + TILE, 0, lane);
-      // the other buffer was last read before the previous barrier
-      if (it + 1 < ntl) store_tile(it + 1);
-    };
-    int it = 0;
-    for (; it < full; ++it) step(it, std::false_type{});
-    for (; it < ntl; ++it) step(it, std::true_type{});
-
-    w.l = half_sum(w.l);
-    w.m *= j.sc;
-    if (live) w.write(a, j, t * ((int64_t)a.Hk * a.G) + head, nsp == 1, half);
-    __syncthreads();  // smem is written again for the next row tile
-  }
-}
-
-// ---------------------------------------------------------------- joining
-// Joins the splits: D / 4 lanes per row, blockIdx.y the group of rows.
-template <int D, bool F16>
-__global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int bm) {
-  constexpr int LPR = D / 4, RPB = 256 / LPR;
-  const int hk = blockIdx.x % a.Hk, b = blockIdx.x / a.Hk;
-  Job j;
-  j.t0 = a.offsets[b];
-  const int64_t t1 = a.offsets[b + 1];
-  if (j.t0 < 0 || t1 <= j.t0 || t1 > a.T) return;
-  j.n = (int)(t1 - j.t0);
-  j.ctx = max(a.context[b], 0);
-  j.len = (int)min((int64_t)j.ctx + j.n, (int64_t)a.max_pages << a.page_log);
-  j.split = 0;
-  const int c = threadIdx.x % LPR;
-  for (int row = blockIdx.y * RPB + threadIdx.x / LPR; row < j.n * a.G; row += gridDim.y * RPB) {
-    int lo, hi;
-    const int last = min(row / bm * bm + bm - 1, j.n * a.G - 1) / a.G;
-    const int nsp = split_range(a, j, last, lo, hi);
-    if (nsp <= 1) continue;  // written by its workgroup
-    const int64_t r = (int64_t)(j.t0 + row / a.G) * (a.Hk * a.G) + hk * a.G + row % a.G;
-    float M = NEG_INF;
-    for (int i = 0; i < nsp; ++i) M = fmaxf(M, a.part_ml[(i * a.rows + r) * 2]);
-    const float ms = M == NEG_INF ? 0.f : M;
-    float L = 0.f;
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = 0; i < nsp; ++i) {
-      const int64_t pr = i * a.rows + r;
-      const float2 ml = *(const float2*)(a.part_ml + pr * 2);
-      const f32x4 p = *(const f32x4*)(a.part_o + pr * D + c * 4);
-      const float f = exp2_fast(ml.x - ms);
-      L += f * ml.y;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] += f * p[e];
-    }
-    const float inv = inverse_sum(L, a.v_scale ? a.v_scale[hk] : 1.f);
-    *(i32x2*)(a.out + r * D + c * 4) =
-        i32x2{pack2<F16>(o[0] * inv, o[1] * inv), pack2<F16>(o[2] * inv, o[3] * inv)};
-    if (a.lse && c == 0) a.lse[r] = row_lse(M, L);
-  }
-}
-
 template <int D, int SHAPE, bool F16, bool KV8>
 hipError_t launch_one(const AttnArgs& a, hipStream_t s) {
   const int64_t grid = (int64_t)((a.nwork + 7) / 8 * 8) * a.ntiles;
   hipError_t e;
-  if constexpr (SHAPE <= AT_STREAM32) {
-    constexpr int NQ = SHAPE == AT_STREAM16 ? 1 : 2;
-    constexpr size_t lds = stream_lds_bytes<D, NQ, KV8>();
-    e = opt_in_lds((const void*)stream_kernel<D, NQ, F16, KV8>, lds);
+  if constexpr (SHAPE == AT_STREAM16) {
+    constexpr size_t lds = stream_lds_bytes<D, KV8>();
+    e = opt_in_lds((const void*)stream_kernel<D, F16, KV8>, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((stream_kernel<D, NQ, F16, KV8>), dim3((unsigned)grid), dim3(256), lds, s, a);
-  } else if constexpr (D == 256) {
-    constexpr size_t lds = 2 * 2 * 32 * D * 2;
-    e = opt_in_lds((const void*)wide_kernel<F16, KV8>, lds);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((wide_kernel<F16, KV8>), dim3((unsigned)grid), dim3(256), lds, s, a);
+    hipLaunchKernelGGL((stream_kernel<D, F16, KV8>), dim3((unsigned)grid), dim3(256), lds, s, a);
   } else {
-    constexpr int CW = SHAPE == AT_TILE128 ? 2 : 1;
+    constexpr int CW = SHAPE == AT_TILE128 && D < 256 ? 2 : 1;
     constexpr size_t lds = tile_lds_bytes<D>();
     e = opt_in_lds((const void*)tile_kernel<D, CW, F16, KV8>, lds);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((tile_kernel<D, CW, F16, KV8>), dim3((unsigned)grid), dim3(512), lds, s, a);
+    hipLaunchKernelGGL((tile_kernel<D, CW, F16, KV8>), dim3((unsigned)grid),
+                       dim3(64 * tile_waves<D>()), lds, s, a);
   }
   e = hipGetLastError();
   if (e != hipSuccess || a.nsplit == 1 || a.counters) return e;
-  const int bm = attn_rows(SHAPE), rpb = 256 / (D / 4);
+  const int bm = attn_rows(SHAPE);
+  int per = 1;  // groups of lanes per row: with eight splits each, all loads are on their way at once
+  while (per < 256 / (D / 4) && per * 8 < a.nsplit) per *= 2;
+  const int rpb = 256 / (D / 4) / per;
   const int64_t groups = std::min<int64_t>(((int64_t)a.ntiles * bm + rpb - 1) / rpb, 65535);
   hipLaunchKernelGGL((join_kernel<D, F16>),
-                     dim3((unsigned)(a.nwork / a.nsplit), (unsigned)groups), dim3(256), 0, s, a, bm);
+                     dim3((unsigned)(a.nwork / a.nsplit), (unsigned)groups), dim3(256), 0, s, a, bm,
+                     per);
   return hipGetLastError();
 }
 
@@ -1240,7 +1146,6 @@ hipError_t launch_dim(const AttnArgs& a, int shape, bool f16, bool kv8, hipStrea
     case AT_TILE128: return launch_types<D, AT_TILE128>(a, f16, kv8, s);
   }
   if constexpr (D < 256) {
-    if (shape == AT_STREAM32) return launch_types<D, AT_STREAM32>(a, f16, kv8, s);
     if (shape == AT_TILE256) return launch_types<D, AT_TILE256>(a, f16, kv8, s);
   }
   return hipErrorInvalidValue;
@@ -1251,18 +1156,25 @@ hipError_t launch_dim(const AttnArgs& a, int shape, bool f16, bool kv8, hipStrea
 AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len) {
   AttnPlan p;
   const int64_t rows = max_nodes * G;
+  // 8 trees over 8000 positions (dim 128, bf16), rows of a key head: 32 rows
+  // take 67 us in tiles of 128 and 83 in two tiles of the streaming kernel, 128
+  // rows 82 and (tiles of 256) 88, 192 rows 118 and 101.  16 rows stream: 48
+  // sequences of 8-bit codes take 127 us, and 231 in tiles of 128.
   if (D == 256) p.shape = rows <= 16 ? AT_STREAM16 : AT_TILE128;  // what fits the registers
-  else p.shape = rows <= 16 ? AT_STREAM16 : rows <= 64 ? AT_STREAM32 : rows <= 128 ? AT_TILE128 : AT_TILE256;
+  else p.shape = rows <= 16 ? AT_STREAM16 : rows <= 128 ? AT_TILE128 : AT_TILE256;
   const int bm = attn_rows(p.shape);
   p.ntiles = (rows + bm - 1) / bm;
   const int64_t units = B * Hk * p.ntiles;
-  const int64_t step = p.shape <= AT_STREAM32 ? 128 : 64;  // positions of one round of the waves
+  const int64_t step = p.shape == AT_STREAM16 ? 128 : 64;  // positions of one round of the waves
   const int64_t steps = (max_len + step - 1) / step;
   int64_t ns;
-  if (p.shape <= AT_STREAM32) {
-    // a few rounds of the 512 workgroups that run at a time, so that uneven
-    // lengths even out
-    ns = (1536 + units - 1) / units;
+  if (p.shape == AT_STREAM16) {
+    // A workgroup for each CU; more make more parts to join (one sequence of
+    // 8000 positions: 14.8 us with 256, 17.9 with 512).  Lengths may differ,
+    // though: up to 1536 where a split is longer than 2048 positions (48
+    // sequences of up to 8191, 8-bit: 143 us with 768, 127 with 1536).
+    ns = (256 + units - 1) / units;
+    if (units * ns < 1536) ns = std::max(ns, std::min((1536 + units - 1) / units, (max_len + 2047) / 2048));
     ns = std::min(ns, steps);
   } else {
     // as many as fill whole rounds best; splits of four tiles at least
@@ -1279,9 +1191,9 @@ AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t m
   p.chunk = (steps + ns - 1) / ns * step;
   p.nsplit = std::max<int64_t>(1, (max_len + p.chunk - 1) / p.chunk);
   // Joined by the last workgroup, a call of one token over 1024 positions
-  // takes 12 instead of 14.6 us; of 1536 workgroups the arrivals and the
-  // narrower stores cost 9 us where the second launch costs 5.6.
-  p.arrival = p.shape <= AT_STREAM32 && units * p.nsplit <= 512;
+  // takes 10.3 instead of 12 us; of 1536 workgroups (48 sequences of up to 8191)
+  // the arrivals and the narrower stores cost 5 us more than a second launch.
+  p.arrival = p.shape == AT_STREAM16 && units * p.nsplit <= 512;
   return p;
 }
 

@@ -13,7 +13,10 @@
 // Memory bound: 2 bytes in and out per value.  A head is D / 8 lanes of 16
 // bytes, so its norm is a reduction by lane shuffles and the partner of a
 // half-split pair is another lane of the same group; nothing goes through
-// LDS.
+// LDS.  8191 tokens of 40 heads of 128 values (bf16) take 43 us (3.9 TB/s; a
+// large copy reaches 4.8), 4099 tokens of 32 query and 8 key heads with their
+// values stored to pages 25 us (3.9 TB/s).  A decode step is one chain of
+// latencies: 4 us in the kernel, 8 to 11 with the call around it.
 #include "launch.hpp"
 
 namespace lg {
@@ -26,7 +29,8 @@ constexpr int RP_WAVES = 4;
 // heads of one kind, so that everything that depends on the kind is scalar;
 // wave jobs of a token are its queries, keys and values in turn.  NPT jobs
 // per wave: their loads all go out first, and the token's cosines and sines
-// are read once for them.
+// are read once for them (8191 tokens: 59 us with one job per wave of mixed
+// kinds, 43 with three of one kind each).
 template <bool F16, int LPH, int NPT>
 __global__ __launch_bounds__(RP_THREADS) void heads_kernel(HeadArgs a) {
   constexpr int HPW = 64 / LPH;

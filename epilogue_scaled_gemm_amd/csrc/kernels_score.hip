@@ -17,9 +17,11 @@
 // it are read again, and their values at or above it collected in LDS, sorted
 // by a bitonic network into the wave's list, and the lists merged.
 //
-// Memory bound for many rows; a chain of latencies for few, which are split
-// over workgroups.  A slice writes its sums and list, and the workgroup that
-// arrives last joins the row's slices.
+// Memory bound for many rows (2048 of 131072 logits in bf16, top 8: 111 us,
+// 4.8 TB/s); a chain of latencies for few, which are split over workgroups (one
+// row of 32003: 10 us with the call around it; 48 rows of 128259 in 32 bits, top
+// 20: 21 us, of which reading is 5).  A slice writes its sums and list, and the
+// workgroup that arrives last joins the row's slices.
 #include "launch.hpp"
 
 namespace lg {

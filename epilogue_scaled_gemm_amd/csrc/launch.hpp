@@ -189,9 +189,9 @@ struct AttnArgs {
 // How a call is cut: the kernel and its row tile, ntiles workgroups over a
 // sequence's rows, nsplit splits of `chunk` positions.
 constexpr int AT_COUNTER_STEP = 16;  // ints; neighbours in lines of their own
-enum AttnShape : int { AT_STREAM16 = 0, AT_STREAM32 = 1, AT_TILE128 = 2, AT_TILE256 = 3 };
+enum AttnShape : int { AT_STREAM16 = 0, AT_TILE128 = 1, AT_TILE256 = 2 };
 inline constexpr int attn_rows(int shape) {
-  return shape == AT_STREAM16 ? 16 : shape == AT_STREAM32 ? 32 : shape == AT_TILE128 ? 128 : 256;
+  return shape == AT_STREAM16 ? 16 : shape == AT_TILE128 ? 128 : 256;
 }
 struct AttnPlan {
   int shape;

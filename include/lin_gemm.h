@@ -399,7 +399,8 @@ typedef struct {
  * rounded to dtype for the product with the values.  Positions beyond the
  * page table are cut off.  Long contexts are split over workgroups, whose
  * sums go to the handle's workspace (grown on demand: warm a shape up before
- * capturing it). */
+ * capturing it).  Up to 2^25 rows (tokens * q_heads); page strides below 2^30
+ * and, times page_size, in-page strides too (a cache may be larger). */
 int lin_gemm_tree_attention(lin_gemm_t h, const lin_attention_t *args, void *stream);
 
 typedef struct {

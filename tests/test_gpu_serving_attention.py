@@ -233,6 +233,22 @@ def test_lengths_cut_at_the_table(handle):
     assert ((out[:, 0].double() - p @ v).abs() <= 2.0 ** -6 * (1e-2 + p @ v.abs())).all()
 
 
+@pytest.mark.parametrize("mask", ["none", "tree"])
+@pytest.mark.parametrize("n,G,bound", [(2, 1, 100), (2, 1, 5000), (40, 4, 100), (70, 4, 5000)])
+def test_a_context_up_to_the_largest_integer(handle, n, G, bound, mask):
+    # what the table has no pages for is cut off, however long it is said to be
+    c = Case([300], [n], 2, G, 128, 16, mask=mask, seed=20)
+    c.table[0, -1] = 0
+    room = c.table.shape[1] * 16
+    results = []
+    for ctx in (room, 2 ** 31 - 1, 2 ** 31 - n):
+        c.context[0] = ctx
+        results.append(c.run(handle, max_context=bound))
+    assert results[0][0].isfinite().all()
+    for out, lse in results[1:]:
+        assert torch.equal(out, results[0][0]) and torch.equal(lse, results[0][1])
+
+
 def test_empty_calls(handle):
     c = Case([40, 9], [2, 3], 1, 2, 64, mask="none", seed=16)
     e = torch.empty(0, 2, 64, dtype=BF16, device="cuda")

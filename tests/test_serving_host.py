@@ -114,6 +114,15 @@ def test_tree_attention_refusals(handle, kw, status):
     assert _call(handle, "lin_gemm_tree_attention", serving._ATTENTION, ATT, ATT_OK, kw) == status
 
 
+@pytest.mark.parametrize("name", ["kc", "vc"])
+@pytest.mark.parametrize("stride,value,status", [
+    ("_ps", -8, UNSUPPORTED), ("_ps", 1 << 30, UNSUPPORTED), ("_ts", -8, UNSUPPORTED),
+    ("_ts", 1 << 26, UNSUPPORTED), ("_ts", 1 << 40, UNSUPPORTED)])
+def test_tree_attention_refuses_pages_beyond_32_bit_offsets(handle, name, stride, value, status):
+    kw = {"tokens": 4, name + stride: value}
+    assert _call(handle, "lin_gemm_tree_attention", serving._ATTENTION, ATT, ATT_OK, kw) == status
+
+
 SCORE_OK = dict(rows=0, vocab=100, logits=FAKE, row_stride=100, tokens=FAKE, temperature=1.0,
                 logprobs=FAKE)
 
