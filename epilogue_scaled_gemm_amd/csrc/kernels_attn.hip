@@ -249,10 +249,10 @@ __device__ inline void join(Part& x, const Part& y) {
 }
 
 // A workgroup joins rows: D / 4 lanes hold one, `per` such groups take its
-// splits in turn with eight on their way, and the groups' sums meet in LDS.
+// splits in turn with AHEAD on their way, and the groups' sums meet in LDS.
 // `r` and `nsp` are the row of this thread and its splits (0: no row).  What
 // other workgroups of the same launch wrote is read with agent-scope loads.
-template <int D, bool F16, bool SAME_LAUNCH>
+template <int D, bool F16, bool SAME_LAUNCH, int AHEAD>
 __device__ ALWAYS_INLINE void join_rows(const AttnArgs& a, int64_t r, int nsp, int per, float vscale,
                                         Part* parts) {
   constexpr int LPR = D / 4;
@@ -261,36 +261,38 @@ __device__ ALWAYS_INLINE void join_rows(const AttnArgs& a, int64_t r, int nsp, i
     if constexpr (SAME_LAUNCH) return __builtin_bit_cast(float2, ld_agent((const double*)q));
     else return *(const float2*)q;
   };
+  auto four = [&](const float* q) {
+    if constexpr (!SAME_LAUNCH) return *(const f32x4*)q;
+    const float2 u = pair(q), v = pair(q + 2);
+    return f32x4{u.x, u.y, v.x, v.y};
+  };
   Part x = {{0.f, 0.f, 0.f, 0.f}, NEG_INF, 0.f};
 #pragma unroll 1
-  for (int i0 = g; i0 < nsp; i0 += 8 * per) {
-    float2 ml[8], u[8], v[8];
+  for (int i0 = g; i0 < nsp; i0 += AHEAD * per) {
+    float2 ml[AHEAD];
+    f32x4 u[AHEAD];
     float m = x.m;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < AHEAD; ++i) {
       ml[i] = make_float2(NEG_INF, 0.f);
       if (i0 + i * per >= nsp) continue;
       const int64_t pr = (int64_t)(i0 + i * per) * a.rows + r;
       ml[i] = pair(a.part_ml + pr * 2);
-      u[i] = pair(a.part_o + pr * D + c4);
-      v[i] = pair(a.part_o + pr * D + c4 + 2);
+      u[i] = four(a.part_o + pr * D + c4);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, ml[i].x);
+    for (int i = 0; i < AHEAD; ++i) m = fmaxf(m, ml[i].x);
     const float ms = m == NEG_INF ? 0.f : m;
     const float f0 = exp2_fast(x.m - ms);
     x.m = m;
     x.l *= f0;
     x.o *= f0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < AHEAD; ++i) {
       if (i0 + i * per >= nsp) continue;
       const float f = exp2_fast(ml[i].x - ms);
       x.l += f * ml[i].y;
-      x.o[0] += f * u[i].x;
-      x.o[1] += f * u[i].y;
-      x.o[2] += f * v[i].x;
-      x.o[3] += f * v[i].y;
+      x.o += f * u[i];
     }
   }
   if (per > 1) {
@@ -308,7 +310,9 @@ __device__ ALWAYS_INLINE void join_rows(const AttnArgs& a, int64_t r, int nsp, i
 }
 
 // After a launch whose splits were left apart: blockIdx.y the group of rows.
-template <int D, bool F16>
+// With many rows it is bound by issue: 96000 rows of two splits (dim 128) take
+// 25 us with two splits ahead and 36 with room for eight.
+template <int D, bool F16, int AHEAD>
 __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int bm, int per) {
   __shared__ Part parts[256];
   const int rows = 256 / (D / 4) / per;  // of a workgroup
@@ -332,7 +336,7 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int bm, int per) 
       if (nsp == 1) nsp = 0;  // written by its workgroup
       r = (int64_t)(j.t0 + row / a.G) * (a.Hk * a.G) + hk * a.G + row % a.G;
     }
-    join_rows<D, F16, false>(a, r, nsp, per, vscale, parts);
+    join_rows<D, F16, false, AHEAD>(a, r, nsp, per, vscale, parts);
   }
 }
 
@@ -656,7 +660,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
     const int g = threadIdx.x / (D / 4);
     for (int r0 = row0; r0 < end; r0 += 256 / (D / 4) / per) {
       const int row = r0 + g / per;
-      join_rows<D, F16, true>(a, row < end ? row_of(row) : 0, row < end ? nsp : 0, per, vscale,
+      join_rows<D, F16, true, 8>(a, row < end ? row_of(row) : 0, row < end ? nsp : 0, per, vscale,
                               (Part*)smem);
     }
     if (threadIdx.x == 0) st_agent(counter, 0);  // kept at zero between calls
@@ -1127,9 +1131,11 @@ hipError_t launch_one(const AttnArgs& a, hipStream_t s) {
   while (per < 256 / (D / 4) && per * 8 < a.nsplit) per *= 2;
   const int rpb = 256 / (D / 4) / per;
   const int64_t groups = std::min<int64_t>(((int64_t)a.ntiles * bm + rpb - 1) / rpb, 65535);
-  hipLaunchKernelGGL((join_kernel<D, F16>),
-                     dim3((unsigned)(a.nwork / a.nsplit), (unsigned)groups), dim3(256), 0, s, a, bm,
-                     per);
+  const dim3 join_grid((unsigned)(a.nwork / a.nsplit), (unsigned)groups);
+  if (a.nsplit == 2)
+    hipLaunchKernelGGL((join_kernel<D, F16, 2>), join_grid, dim3(256), 0, s, a, bm, per);
+  else
+    hipLaunchKernelGGL((join_kernel<D, F16, 8>), join_grid, dim3(256), 0, s, a, bm, per);
   return hipGetLastError();
 }
 
