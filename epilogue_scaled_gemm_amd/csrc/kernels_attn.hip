@@ -670,12 +670,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
 // ------------------------------------------------------------ many rows
 // A tile in LDS holds its rows as 16-byte chunks; the chunk index is XOR-ed
 // with the row so that 32 lanes that read one chunk of 32 rows (K) or four
-// rows of two chunks (V, transposing reads) use all banks.
+// rows of four chunks (V, transposing reads) use all banks, of which a row of
+// 64 values covers half.  (No conflicts are counted; with the row shifted by
+// one for V at dim 128 and 256 there were two cycles of them per transposing
+// read, which cost 4 to 8% at dim 256 and 1% at most at 128.)
 template <int D> __device__ inline int k_off(int row, int chunk) {
   return row * (D * 2) + ((chunk ^ (row & (D / 8 - 1))) << 4);
 }
+template <int D> __device__ inline int v_xor(int row) {
+  return (row << (D == 64 ? 1 : 2)) & (D / 8 - 1);
+}
 template <int D> __device__ inline int v_off(int row, int chunk) {
-  return row * (D * 2) + ((chunk ^ ((row << 1) & (D / 8 - 1))) << 4);
+  return row * (D * 2) + ((chunk ^ v_xor<D>(row)) << 4);
 }
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -878,9 +884,9 @@ template <int D> constexpr int tile_lds_bytes() { return TILE_BUFS * tile_positi
 // way into LDS alone takes 103 (5.1 TB/s) and the arithmetic alone 143 (0.94
 // PFLOP/s); 1500 nodes over 5001: 0.86 PFLOP/s.
 // Dim 256 has four waves, one per SIMD: O and Q of 32 rows take 200 registers.
-// 16 trees of 64 nodes over 2000 positions: 182 us (0.37 PFLOP/s: nothing runs
-// beside a wave's exponentials), and 208 with the LDS offsets of the fragments
-// kept over the loop, for which O went to memory.
+// 16 trees of 64 nodes over 2000 positions: 175 us (0.38 PFLOP/s: nothing runs
+// beside a wave's exponentials), and 25 more with the LDS offsets of the
+// fragments kept over the loop, for which O went to memory.
 // Measured and not kept:
 // strict alternation of the two waves between barriers (215 us), the first
 // product of the next block inside the softmax of this one (spills), fragments
@@ -977,7 +983,7 @@ __global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(AttnArgs a) 
           char* const at = sk + (wave * NI + i) * 1024;
           __builtin_amdgcn_global_load_lds((global_void*)(ka + ((c ^ (r & (CPR - 1))) << 4)),
                                            (lds_void*)at, 16, 0, 0);
-          __builtin_amdgcn_global_load_lds((global_void*)(va + ((c ^ ((r << 1) & (CPR - 1))) << 4)),
+          __builtin_amdgcn_global_load_lds((global_void*)(va + ((c ^ v_xor<D>(r)) << 4)),
                                            (lds_void*)(at + TILE), 16, 0, 0);
         }
       }
