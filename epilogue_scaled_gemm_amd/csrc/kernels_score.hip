@@ -170,7 +170,9 @@ template <int ET> __device__ inline float load_one(const void* p, int64_t i) {
   else return h_to_f32<ET == 1>(((const uint16_t*)p)[i]);
 }
 
-// A row's results.
+// A row's results.  A row with NaN can have fewer values in order than places:
+// those that are left hold their own number for an index (k is at most the
+// vocabulary's size), and the key 0 stands for NaN.
 template <int ET>
 __device__ inline void write_row(const ScoreArgs& a, int64_t t, Sums r, uint64_t list, int lane) {
   const float ls = __builtin_amdgcn_logf(r.s);  // log2
@@ -186,7 +188,7 @@ __device__ inline void write_row(const ScoreArgs& a, int64_t t, Sums r, uint64_t
     if (a.entropy) a.entropy[t] = (ls - r.w / r.s) * LN2;
   }
   if (lane < a.k) {
-    if (a.top_ids) a.top_ids[t * a.k + lane] = (int)~(uint32_t)list;
+    if (a.top_ids) a.top_ids[t * a.k + lane] = list ? (int)~(uint32_t)list : lane;
     if (a.top_logprobs) a.top_logprobs[t * a.k + lane] = logprob(key_value(list));
   }
 }
