@@ -112,8 +112,10 @@ __device__ inline float at_least(float mx, int k, int lane) {
 // Sums of one lane, wave or slice, relative to the maximum m (a logit).
 // Exponents are base 2: a value's is x c - M with c = log2(e) / temperature and
 // M = m c, rounded; the product x c is exact in the FMA, so the difference is
-// rounded once, however far the logits lie from zero.  Where m c is beyond
-// what that can hold, it is (x - m) c.
+// rounded once.  All of them are then off by what M was rounded by, which
+// cancels in the results as long as it is no large exponent itself: it is
+// below one for M up to 2^24.  Beyond that (logits that an additive mask has
+// moved far from zero) exponents are (x - m) c.
 struct Sums {
   float m, s, w;
 };
@@ -122,7 +124,7 @@ __device__ inline float frame(float m, float c) {
   asm volatile("" : "+v"(mc));  // rounded here: never part of another FMA
   return mc;
 }
-__device__ inline bool in_range(float mc) { return fabsf(mc) < 1e30f; }
+__device__ inline bool in_range(float mc) { return fabsf(mc) < 16777216.f; }
 __device__ inline float rel(float x, float m, float c) {
   const float mc = frame(m, c);
   return in_range(mc) ? fmaf(x, c, -mc) : (x - m) * c;
