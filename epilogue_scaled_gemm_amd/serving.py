@@ -315,11 +315,15 @@ def tree_mask(parents, device="cuda"):
 
 def node_slots(page_table, context, offsets, page_size):
     """Cache slots int32 [T] of the nodes: node j of sequence b at position
-    context[b] + j of its pages.  Elementary torch operations on the plans'
+    context[b] + j of its pages, or -1 (not stored) past the page table and
+    at table entries below 0.  Elementary torch operations on the plans'
     device; T comes from offsets[-1]."""
     T = int(offsets[-1])
     t = torch.arange(T, device=offsets.device)
     b = torch.searchsorted(offsets[1:].contiguous(), t.to(offsets.dtype), right=True)
     pos = context[b].long() + t - offsets[b].long()
-    page = page_table[b, pos // page_size].long()
-    return (page * page_size + pos % page_size).to(torch.int32)
+    at = pos // page_size
+    last = page_table.shape[1] - 1
+    page = page_table[b, at.clamp(0, last)].long()
+    slot = page * page_size + pos % page_size
+    return torch.where((at >= 0) & (at <= last) & (page >= 0), slot, -1).to(torch.int32)
