@@ -21,6 +21,7 @@ namespace {
 // Launches stay below 2^32 threads.
 constexpr int64_t kMaxTokens = (int64_t)1 << 23;
 constexpr int64_t kMaxGroups = (int64_t)1 << 23;
+constexpr double kLog2e = 1.4426950408889634;
 
 bool bad4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3) != 0; }
 
@@ -195,7 +196,8 @@ int run_attention(lin_gemm_t h, const lin_attention_t* p, hipStream_t s) {
     return fail(h, LIN_ERR_UNSUPPORTED, "more than 2^23 tokens, 4096 heads or 65535 sequences");
   if (p->tokens > ((int64_t)1 << 25) / p->q_heads)
     return fail(h, LIN_ERR_UNSUPPORTED, "more than 2^25 rows of one head");
-  if (!std::isfinite(p->scale)) return fail(h, LIN_ERR_INVALID_ARG, "scale must be finite");
+  if (!std::isfinite((float)(p->scale * kLog2e)))  // (what the kernels hold)
+    return fail(h, LIN_ERR_INVALID_ARG, "scale must be finite, in binary32 too");
   int rc = check_cache(h, p->dtype, p->cache_type, p->pages, p->page_size, p->k_cache, p->v_cache,
                        {p->k_page_stride, p->k_head_stride, p->k_in_page_stride, p->v_page_stride,
                         p->v_head_stride, p->v_in_page_stride});
@@ -255,7 +257,7 @@ int run_attention(lin_gemm_t h, const lin_attention_t* p, hipStream_t s) {
   a.pages = (int)p->pages;
   a.page_log = log2_exact(p->page_size);
   a.page_mask = (int)p->page_size - 1;
-  a.scale_log2e = (float)(p->scale * 1.4426950408889634);
+  a.scale_log2e = (float)(p->scale * kLog2e);
   // The bounds shape the launch: at least one node and one position, at most
   // what the tensors can hold.
   const int64_t nodes = std::min(std::max<int64_t>(p->max_nodes, 1), p->tokens);
@@ -291,8 +293,12 @@ int run_score(lin_gemm_t h, const lin_score_t* p, hipStream_t s) {
     return fail(h, LIN_ERR_INVALID_ARG, "dtype must be 0 (bf16), 1 (fp16) or 2 (fp32)");
   if (p->rows < 0 || p->vocab < 0 || p->top < 0)
     return fail(h, LIN_ERR_INVALID_ARG, "negative size");
-  if (!(p->temperature > 0) || !std::isfinite(p->temperature))
-    return fail(h, LIN_ERR_INVALID_ARG, "temperature must be positive and finite");
+  // its inverse is a factor of the logits: an infinite one would make NaN of
+  // the largest, one of zero of those that are masked with -inf
+  const float per_logit = (float)(kLog2e / p->temperature);
+  if (!(per_logit > 0) || !std::isfinite(per_logit))
+    return fail(h, LIN_ERR_INVALID_ARG,
+                "temperature must be positive, and log2(e) over it within binary32");
   if (p->top > lg::SCORE_MAX_TOP || p->top > p->vocab)
     return fail(h, LIN_ERR_UNSUPPORTED, "top must be at most 32 and at most vocab");
   if (p->rows > kMaxTokens || p->vocab > ((int64_t)1 << 30))
@@ -317,7 +323,7 @@ int run_score(lin_gemm_t h, const lin_score_t* p, hipStream_t s) {
   a.V = p->vocab;
   a.stride = p->row_stride;
   a.k = p->top_ids || p->top_logprobs ? (int)p->top : 0;
-  a.c = (float)(1.4426950408889634 / p->temperature);
+  a.c = per_logit;
   a.inv_t = (float)(1.0 / p->temperature);
   lg::score_plan(a.T, a.V, (int)p->dtype, &a.nsplit, &a.slice);
   if (a.nsplit > 1) {

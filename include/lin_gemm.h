@@ -381,7 +381,8 @@ typedef struct {
                                  they shape the launch, any lengths are right */
     const int64_t *mask;      /* [tokens][mask_words] or NULL                 */
     int64_t mask_words;
-    double scale;             /* of the scores                                */
+    double scale;             /* of the scores, finite (times log2(e), in
+                                 binary32)                                    */
     void *out;                /* [tokens][q_heads][dim], contiguous           */
     float *lse;               /* [tokens][q_heads] or NULL                    */
 } lin_attention_t;
@@ -409,7 +410,7 @@ typedef struct {
     const void *logits;       /* [rows][vocab], row_stride elements apart     */
     int64_t row_stride;
     const int32_t *tokens;    /* [rows]                                       */
-    double temperature;       /* > 0                                          */
+    double temperature;       /* > 0; log2(e) over it within binary32       */
     float *logprobs;          /* [rows]                                       */
     float *entropy;           /* [rows] or NULL                               */
     int64_t top;              /* 0 .. 32, at most vocab                       */
