@@ -222,17 +222,31 @@ __device__ inline i32x4 scaled_q(i32x4 q, bool flip, bool zero) {
   return q;
 }
 
-// The running maximum moves only when it grows by more than 2^8 for some row
-// of the wave: until then the weights stay below 2^8 of the kept one, which
-// costs no precision, and the sums need no rescaling.
-constexpr float SLACK = 8.f;
+// The running maximum moves only when it grows by more than 2^SLACK for some
+// row of the wave: until then the weights stay below that, and the sums need
+// no rescaling.  bf16 weights have binary32's range, so 2^8 costs no precision.
+// fp16 ones lose bits below 2^-14 and vanish below 2^-25, which many positions
+// beside a heavy one add up to (results made of such weights were off by 900
+// times the bound): theirs carry a factor of 2^LIFT, as their sum does, so that
+// 2^SLACK is just within the type and bits are lost only below 2^-25.  (A slack
+// of 2 and a lift of 13 would move that to 2^-27, but rescales more often: 1500
+// nodes over 5001 positions 375 us against 368, dim 256 1126 against 1080.)
+template <bool F16> constexpr float SLACK = F16 ? 4.f : 8.f;
+template <bool F16> constexpr float LIFT = F16 ? 11.f : 0.f;
+
+// What is added to a row's scores (base 2) before the exponential.
+template <bool F16> __device__ inline float weight_offset(float m, float sc) {
+  const float ms = m == NEG_INF ? 0.f : m * sc;
+  if constexpr (F16) return LIFT<F16> - ms;
+  else return -ms;
+}
 
 // O / l, rounded, and the row's lse from m (base 2) and l.
 __device__ inline float inverse_sum(float l, float vscale) {
   return l > 0.f || l != l ? vscale / l : 0.f;
 }
-__device__ inline float row_lse(float m, float l) {
-  return (m + __builtin_amdgcn_logf(l)) * 0.69314718056f;
+template <bool F16> __device__ inline float row_lse(float m, float l) {
+  return (m + (__builtin_amdgcn_logf(l) - LIFT<F16>)) * 0.69314718056f;
 }
 
 // ------------------------------------------------------ joining the splits
@@ -306,7 +320,7 @@ __device__ ALWAYS_INLINE void join_rows(const AttnArgs& a, int64_t r, int nsp, i
   const float inv = inverse_sum(x.l, vscale);
   *(i32x2*)(a.out + r * D + c4) =
       i32x2{pack2<F16>(x.o[0] * inv, x.o[1] * inv), pack2<F16>(x.o[2] * inv, x.o[3] * inv)};
-  if (a.lse && c4 == 0) a.lse[r] = row_lse(x.m, x.l);
+  if (a.lse && c4 == 0) a.lse[r] = row_lse<F16>(x.m, x.l);
 }
 
 // After a launch whose splits were left apart: blockIdx.y the group of rows.
@@ -511,7 +525,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
 #pragma unroll
       for (int i = 1; i < 8; ++i) mx = fmaxf(mx, s[i >> 2][i & 3]);
       const float mn = fmaxf(m, quad_max(mx));
-      if (__any((mn - m) * j.sc > SLACK)) {
+      if (__any((mn - m) * j.sc > SLACK<F16>)) {
         const float f = mn == NEG_INF ? 1.f : exp2_fast((m - mn) * j.sc);
         m = mn;
         l *= f;
@@ -520,11 +534,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[dt][i] *= f;
       }
-      const float ms = m == NEG_INF ? 0.f : m * j.sc;
+      const float at = weight_offset<F16>(m, j.sc);
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        s[i >> 2][i & 3] = exp2_fast(fmaf(s[i >> 2][i & 3], j.sc, -ms));
+        s[i >> 2][i & 3] = exp2_fast(fmaf(s[i >> 2][i & 3], j.sc, at));
         sum += s[i >> 2][i & 3];
       }
       l += sum;
@@ -619,7 +633,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
           *(i32x2*)(a.out + r * D + dt * 16 + grp * 4) =
               i32x2{pack2<F16>(o[dt][0] * inv, o[dt][1] * inv),
                     pack2<F16>(o[dt][2] * inv, o[dt][3] * inv)};
-        if (a.lse && grp == 0) a.lse[r] = row_lse(m, l);
+        if (a.lse && grp == 0) a.lse[r] = row_lse<F16>(m, l);
       } else if (!a.counters) {
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) *(f32x4*)(a.part_o + pr * D + dt * 16 + grp * 4) = o[dt];
@@ -757,7 +771,7 @@ template <int D, bool F16> struct Rows {
 #pragma unroll
     for (int i = 1; i < 16; ++i) mx = fmaxf(mx, p[i]);
     const float mn = fmaxf(m, half_max(mx));
-    if (__any((mn - m) * j.sc > SLACK)) {
+    if (__any((mn - m) * j.sc > SLACK<F16>)) {
       const float f = mn == NEG_INF ? 1.f : exp2_fast((m - mn) * j.sc);
       m = mn;
       l *= f;
@@ -766,11 +780,11 @@ template <int D, bool F16> struct Rows {
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[dt][i] *= f;
     }
-    const float ms = m == NEG_INF ? 0.f : m * j.sc;
+    const float at = weight_offset<F16>(m, j.sc);
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      p[i] = exp2_fast(fmaf(p[i], j.sc, -ms));
+      p[i] = exp2_fast(fmaf(p[i], j.sc, at));
       sum += p[i];
     }
     l += sum;
@@ -832,7 +846,7 @@ template <int D, bool F16> struct Rows {
           *(i32x2*)(op + dt * 32 + b * 8) =
               i32x2{pack2<F16>(o[dt][b * 4] * inv, o[dt][b * 4 + 1] * inv),
                     pack2<F16>(o[dt][b * 4 + 2] * inv, o[dt][b * 4 + 3] * inv)};
-      if (a.lse && half == 0) a.lse[r] = row_lse(m, l);
+      if (a.lse && half == 0) a.lse[r] = row_lse<F16>(m, l);
     } else {
       const int64_t pr = (int64_t)j.split * a.rows + r;
       float* const op = a.part_o + pr * D + half * 4;

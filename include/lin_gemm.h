@@ -397,7 +397,8 @@ typedef struct {
  * that sees nothing, or only scores of -inf, gets zeros and an lse of -inf.
  * Positions a row does not see do not reach it, infinities and NaN there
  * included.  Scores, sums and lse are binary32; the probabilities are
- * rounded to dtype for the product with the values.  Positions beyond the
+ * rounded to dtype for the product with the values (fp16: below 2^-25 of the
+ * row's largest with fewer bits).  Positions beyond the
  * page table are cut off.  Long contexts are split over workgroups, whose
  * sums go to the handle's workspace (grown on demand: warm a shape up before
  * capturing it).  Up to 2^25 rows (tokens * q_heads); page strides below 2^30
