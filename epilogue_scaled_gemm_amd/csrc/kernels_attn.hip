@@ -234,19 +234,109 @@ __device__ inline i32x4 scaled_q(i32x4 q, bool flip, bool zero) {
 template <bool F16> constexpr float SLACK = F16 ? 4.f : 8.f;
 template <bool F16> constexpr float LIFT = F16 ? 11.f : 0.f;
 
-// What is added to a row's scores (base 2) before the exponential.
-template <bool F16> __device__ inline float weight_offset(float m, float sc) {
-  const float ms = m == NEG_INF ? 0.f : m * sc;
-  if constexpr (F16) return LIFT<F16> - ms;
-  else return -ms;
-}
-
 // O / l, rounded, and the row's lse from m (base 2) and l.
 __device__ inline float inverse_sum(float l, float vscale) {
   return l > 0.f || l != l ? vscale / l : 0.f;
 }
 template <bool F16> __device__ inline float row_lse(float m, float l) {
   return (m + (__builtin_amdgcn_logf(l) - LIFT<F16>)) * 0.69314718056f;
+}
+
+// ------------------------------------------------- rows with far scores
+// A row's exponents are s sc - M with M = m sc, rounded: all of them are off by
+// what M was rounded by, which cancels as long as it is small.  Where M gets to
+// 2^22 (scores of heads near their type's limits) it is not, and sums would
+// overflow or vanish.  Such a row adds nothing up while its maximum is that far
+// (from below zero it may still come back), and if it ends there, far_row
+// computes it again: exponents (s - m) sc, all in 32 bits, one wave for one row, a
+// position per lane for the scores and D / 64 values per lane for the sums.  That
+// takes about 100 times as long.  (Exponents chosen within the kernels' steps
+// cost all calls up to 5%, and a variable more that is carried through the
+// steps up to 20%: they have no register left for it.)
+constexpr float FAR = 4194304.f;
+__device__ inline bool is_far(float ms) { return fabsf(ms) >= FAR && fabsf(ms) < -NEG_INF; }
+
+// What is added to a row's scores (base 2) before the exponential.
+template <bool F16> __device__ inline float weight_offset(float m, float sc) {
+  const float ms = m * sc;
+  return fabsf(ms) < FAR ? LIFT<F16> - ms : NEG_INF;  // (-inf also for m = -inf)
+}
+
+// What the waves of a workgroup read of the cache.
+struct Cache {
+  const char *k, *v;               // of the key head
+  uint32_t k_ps, k_ts, v_ps, v_ts; // page and in-page strides in bytes
+  const int* table;
+};
+
+// The positions [lo, hi) of the row of `node` with the query at `q`; buf, in
+// LDS: D sums, then m (base 2) and l.
+template <int D, bool F16, bool KV8>
+__device__ void far_row(const AttnArgs& a, const Job& j, const Cache& c, const uint16_t* q, int node,
+                        int lo, int hi, float* buf, int lane) {
+  constexpr int VPL = D / 64;
+  const int64_t* const mrow = a.mask ? a.mask + (int64_t)(j.t0 + node) * a.mask_words : nullptr;
+  float m = NEG_INF, l = 0.f, o[VPL] = {};
+#pragma unroll 1
+  for (int base = lo; base < hi; base += 64) {
+    const int pos = min(base + lane, hi - 1);
+    const uint32_t page = min(max(c.table[pos >> a.page_log], 0), a.pages - 1);
+    const char* const kp = c.k + (uint64_t)page * c.k_ps + (pos & a.page_mask) * c.k_ts;
+    float s = 0.f;
+#pragma unroll 1
+    for (int d = 0; d < D; d += 8) {
+      float x[8], y[8];
+      unpack8<F16>(scaled_q(*(const i32x4*)(q + d), j.flip, j.none), x);
+      if constexpr (KV8) {
+        const i32x2 w = *(const i32x2*)(kp + d);
+        unpack8<F16>(widen8<F16>(w[0], w[1]), y);
+      } else {
+        unpack8<F16>(*(const i32x4*)(kp + d * 2), y);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
+    }
+    const bool seen = base + lane < hi && (sees4(a, j, node, mrow, pos, hi) & 1);
+    if (!seen) s = NEG_INF;
+    float mn = s;
+#pragma unroll
+    for (int i = 32; i > 0; i >>= 1) mn = fmaxf(mn, __shfl_xor(mn, i));
+    mn = fmaxf(m, mn);
+    const float f = m == NEG_INF ? 0.f : exp2_fast((m - mn) * j.sc);
+    m = mn;
+    const float e = seen ? exp2_fast(fmaf(s - (m == NEG_INF ? 0.f : m), j.sc, LIFT<F16>)) : 0.f;
+    float sum = e;
+#pragma unroll
+    for (int i = 32; i > 0; i >>= 1) sum += __shfl_xor(sum, i);
+    l = l * f + sum;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) o[i] *= f;
+    for (uint64_t some = __ballot(e != 0.f); some; some &= some - 1) {
+      const int i = __builtin_ctzll(some);
+      const float w = __shfl(e, i);
+      const char* const vp = c.v + (uint64_t)__shfl(page, i) * c.v_ps + (__shfl(pos, i) & a.page_mask) * c.v_ts;
+#pragma unroll
+      for (int k = 0; k < VPL; ++k) {
+        const int d = lane * VPL + k;
+        uint32_t bits;
+        if constexpr (KV8) bits = widen2<F16, false>(((const uint8_t*)vp)[d]);
+        else bits = ((const uint16_t*)vp)[d];
+        o[k] = fmaf(w, h_to_f32<F16>((uint16_t)bits), o[k]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < VPL; ++k) buf[lane * VPL + k] = o[k];
+  if (lane == 0) {
+    buf[D] = m * j.sc;
+    buf[D + 1] = l;
+  }
+}
+// LDS between the lanes of one wave.
+__device__ inline void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // ------------------------------------------------------ joining the splits
@@ -401,6 +491,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
   const char* const vb = (const char*)a.v + j.hk * a.v_hs * ES;
   // a page's bytes fit 32 bits (checked on the host), a cache's need not
   const uint32_t k_ps = a.k_ps * ES, k_ts = a.k_ts * ES, v_ps = a.v_ps * ES, v_ts = a.v_ts * ES;
+  const Cache cache = {kb, vb, k_ps, k_ts, v_ps, v_ts, table};
   const int nrows = j.n * a.G;
 
   for (int tile = j.tile0; tile * 16 < nrows; tile += a.ntiles) {
@@ -617,6 +708,24 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
         for (int dt = 0; dt < DT; ++dt) o[dt] += sums[(wave * DT + dt) * 64 + lane];
       }
       __syncthreads();
+    }
+    if (wave == 0) {
+      uint64_t rows = __ballot(live && is_far(m)) & 0xFFFF;
+      while (__builtin_expect(rows != 0, 0)) {
+        const int r = __builtin_ctzll(rows), row = row0 + r;
+        float* const buf = (float*)smem;
+        far_row<D, F16, KV8>(a, j, cache, a.q + (int64_t)(j.t0 + row / a.G) * a.q_ts +
+                             (int64_t)(j.hk * a.G + row % a.G) * a.q_hs, row / a.G, lo, hi, buf, lane);
+        wave_sync();
+        if (col == r) {
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) o[dt] = *(const f32x4*)(buf + dt * 16 + grp * 4);
+          m = buf[D];
+          l = buf[D + 1];
+        }
+        wave_sync();
+        rows &= rows - 1;
+      }
     }
     const int heads = a.Hk * a.G;
     auto row_of = [&](int row) {  // of q and out
@@ -930,6 +1039,7 @@ __global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(AttnArgs a) 
   const char* const vb = (const char*)a.v + j.hk * a.v_hs * ES;
   // a page's bytes fit 32 bits (checked on the host), a cache's need not
   const uint32_t k_ps = a.k_ps * ES, k_ts = a.k_ts * ES, v_ps = a.v_ps * ES, v_ts = a.v_ts * ES;
+  const Cache cache = {kb, vb, k_ps, k_ts, v_ps, v_ts, table};
   const int nrows = j.n * a.G;
   if (grp) __builtin_amdgcn_s_setprio(1);
 
@@ -1121,6 +1231,31 @@ __global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(AttnArgs a) 
       }
     }
     const Row r = my_row();
+    if (CW == 1 || grp == 0) {
+      uint64_t rows = __ballot(r.live && is_far(w.m)) & 0xFFFFFFFF;
+      // (behind the sums of the second halves, which other waves may still read)
+      float* const buf = (float*)(smem + TILE_BUFS * 2 * TILE) - (wave + 1) * (D + 4);
+      while (__builtin_expect(rows != 0, 0)) {
+        const int i = __builtin_ctzll(rows), row = row0 + rw * 32 + i, ln = again(lane);
+        far_row<D, F16, KV8>(a, j, cache, a.q + (int64_t)(j.t0 + row / a.G) * a.q_ts +
+                             (int64_t)(j.hk * a.G + row % a.G) * a.q_hs, row / a.G, lo, hi, buf, ln);
+        wave_sync();
+        if ((ln & 31) == i) {
+#pragma unroll
+          for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+              const f32x4 x = *(const f32x4*)(buf + dt * 32 + b * 8 + (ln >> 5) * 4);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w.o[dt][b * 4 + e] = x[e];
+            }
+          w.m = buf[D];
+          w.l = buf[D + 1];
+        }
+        wave_sync();
+        rows &= rows - 1;
+      }
+    }
     if (r.live && (CW == 1 || grp == 0))
       w.write(a, j, (int64_t)(j.t0 + r.node) * (a.Hk * a.G) + r.head, nsp == 1, half);
     __syncthreads();  // smem is written again for the next row tile
