@@ -168,10 +168,9 @@ int ensure_workspace(lin_gemm_t h, const lg::Variant& v, const lg::Call& c, int 
     h->ws = nullptr;
     h->ws_bytes = 0;
     size_t bytes = grow_size(need);
-    if (hipMalloc(&h->ws, bytes) != hipSuccess) {
-      h->ws = nullptr;
+    h->ws = lg::device_alloc(bytes);
+    if (!h->ws)
       return fail(h, LIN_ERR_OOM, "split-K workspace allocation of " + std::to_string(bytes) + " bytes failed");
-    }
     h->ws_bytes = bytes;
   }
   if (grow_cnt) {
@@ -179,10 +178,8 @@ int ensure_workspace(lin_gemm_t h, const lg::Variant& v, const lg::Call& c, int 
     h->counters = nullptr;
     h->counters_n = 0;
     size_t n = grow_size(ncnt * sizeof(int)) / sizeof(int);
-    if (hipMalloc(&h->counters, n * sizeof(int)) != hipSuccess) {
-      h->counters = nullptr;
-      return fail(h, LIN_ERR_OOM, "split-K counter allocation failed");
-    }
+    h->counters = (int*)lg::device_alloc(n * sizeof(int));
+    if (!h->counters) return fail(h, LIN_ERR_OOM, "split-K counter allocation failed");
     h->counters_n = n;
     hipError_t e = lg::launch_fill_zero(h->counters, n * sizeof(int), s);
     if (e != hipSuccess) return hip_fail(h, e, "counter zero fill");
@@ -600,10 +597,9 @@ int lin_gemm_run_dynamic(lin_gemm_t h, const void* X, int x_dtype, const void* B
     h->dq = nullptr;
     h->dq_bytes = 0;
     const size_t bytes = grow_size(need);
-    if (hipMalloc(&h->dq, bytes) != hipSuccess) {
-      h->dq = nullptr;
+    h->dq = lg::device_alloc(bytes);
+    if (!h->dq)
       return fail(h, LIN_ERR_OOM, "staging allocation of " + std::to_string(bytes) + " bytes failed");
-    }
     h->dq_bytes = bytes;
   }
   float* sa = (float*)((char*)h->dq + qbytes);

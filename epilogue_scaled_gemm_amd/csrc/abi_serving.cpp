@@ -154,10 +154,9 @@ int ensure_bytes(lin_gemm_t h, size_t need, hipStream_t s) {
   h->ws = nullptr;
   h->ws_bytes = 0;
   const size_t bytes = grow_size(need);
-  if (hipMalloc(&h->ws, bytes) != hipSuccess) {
-    h->ws = nullptr;
+  h->ws = lg::device_alloc(bytes);
+  if (!h->ws)
     return fail(h, LIN_ERR_OOM, "workspace allocation of " + std::to_string(bytes) + " bytes failed");
-  }
   h->ws_bytes = bytes;
   return LIN_OK;
 }
@@ -171,10 +170,8 @@ int ensure_counters(lin_gemm_t h, size_t n, hipStream_t s) {
   h->counters = nullptr;
   h->counters_n = 0;
   const size_t bytes = grow_size(n * sizeof(int));
-  if (hipMalloc(&h->counters, bytes) != hipSuccess) {
-    h->counters = nullptr;
-    return fail(h, LIN_ERR_OOM, "arrival counter allocation failed");
-  }
+  h->counters = (int*)lg::device_alloc(bytes);
+  if (!h->counters) return fail(h, LIN_ERR_OOM, "arrival counter allocation failed");
   e = lg::launch_fill_zero(h->counters, bytes, s);
   if (e != hipSuccess) return hip_fail(h, e, "counter zero fill");
   h->counters_n = bytes / sizeof(int);

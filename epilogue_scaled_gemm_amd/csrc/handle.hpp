@@ -34,8 +34,19 @@ inline int fail(lin_gemm_t h, int status, const std::string& msg) {
   return status;
 }
 
+// An error that a call reports is taken off the runtime's record, where the
+// launch check of the next call would find it.
 inline int hip_fail(lin_gemm_t h, hipError_t e, const char* what) {
+  (void)hipGetLastError();
   return fail(h, LIN_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
+}
+
+// Device memory, or null (with no error on the record).
+inline void* device_alloc(size_t bytes) {
+  void* p = nullptr;
+  if (hipMalloc(&p, bytes) == hipSuccess) return p;
+  (void)hipGetLastError();
+  return nullptr;
 }
 
 // Sizes of handle-owned buffers grow in powers of two (at least 1 MiB), so
