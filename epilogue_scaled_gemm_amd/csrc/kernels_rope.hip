@@ -110,7 +110,30 @@ __global__ __launch_bounds__(RP_THREADS) void heads_kernel(HeadArgs a) {
         for (int e = 0; e < 8; ++e) ss += y[e] * y[e];
 #pragma unroll
         for (int off = LPH / 2; off > 0; off >>= 1) ss += __shfl_xor(ss, off, LPH);
-        const float r = __builtin_amdgcn_rsqf(ss / (float)a.D + a.eps);
+        const float mean = ss / (float)a.D + a.eps;
+        float r = __builtin_amdgcn_rsqf(mean);
+        // Squares that leave binary32's normal range (values beyond 2^60 or, with
+        // next to no eps, below 2^-48): the head times a power of two that
+        // brings the larger of it and the root of eps near one.
+        const bool off = !(mean > 0x1p-96f && mean < 0x1p120f);
+        if (__any(off)) {
+          float big = sqrtf(a.eps);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(y[e]));
+#pragma unroll
+          for (int o = LPH / 2; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor(big, o, LPH));
+          const bool scaled = off && big > 0.f && big < __builtin_inff();
+          const int up = scaled ? -__builtin_amdgcn_frexp_expf(big) : 0;
+          ss = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            y[e] = ldexpf(y[e], up);
+            ss += y[e] * y[e];
+          }
+#pragma unroll
+          for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor(ss, o, LPH);
+          if (scaled) r = __builtin_amdgcn_rsqf(ss / (float)a.D + ldexpf(a.eps, 2 * up));
+        }
         float wf[8];
         i32x4 wr = {0, 0, 0, 0};
         if (c < nch) wr = *(const i32x4*)(w + c * 8);

@@ -346,8 +346,8 @@ typedef struct {
 /* Norms of queries and keys for each head and the position rotation, one
  * pass:  y = x / sqrt(mean(x^2) + eps) * w  where w is given, then each pair
  * (a, b) of the first rope_dim values becomes (a c - b s, b c + a s) with c
- * and s from the table row of the token's position.  Computed in binary32,
- * rounded once.  Outputs may be the inputs themselves (same address and
+ * and s from the table row of the token's position.  Computed in binary32
+ * (heads of any finite size), rounded once.  Outputs may be the inputs themselves (same address and
  * strides), not otherwise overlap them.  kv_heads may be 0. */
 int lin_gemm_qk_norm_rope(lin_gemm_t h, const lin_heads_t *args, void *stream);
 
