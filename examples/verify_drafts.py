@@ -48,7 +48,7 @@ class Layer:
         self.embedding = randn(vocab, hidden).to(BF16)
         self.q_weight = (1 + 0.1 * randn(dim)).to(BF16)
         self.k_weight = (1 + 0.1 * randn(dim)).to(BF16)
-        self.table = lg.rope_table(32768, dim)
+        self.table = lg.rope_table(pages * page, dim)  # no position is beyond the cache
         shape = (pages, kv_heads, page, dim)
         dt = E4M3 if cache8 else BF16
         self.k_cache, self.v_cache = randn(*shape).to(dt), randn(*shape).to(dt)
