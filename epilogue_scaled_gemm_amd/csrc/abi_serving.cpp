@@ -260,7 +260,7 @@ int run_attention(lin_gemm_t h, const lin_attention_t* p, hipStream_t s) {
   const int64_t nodes = std::min(std::max<int64_t>(p->max_nodes, 1), p->tokens);
   const int64_t room = p->max_pages * p->page_size;
   const int64_t len = std::min(std::min(p->max_context, room) + nodes, room);
-  const lg::AttnPlan plan = lg::attn_plan(p->sequences, a.Hk, a.G, (int)p->dim, nodes, len);
+  const lg::AttnPlan plan = lg::attn_plan(p->sequences, a.Hk, a.G, (int)p->dim, nodes, len, a.rows);
   const int64_t work = p->sequences * a.Hk * plan.nsplit;
   if (work > kMaxGroups / plan.ntiles - 8)
     return fail(h, LIN_ERR_UNSUPPORTED, "too many workgroups for one launch");

@@ -1314,7 +1314,8 @@ hipError_t launch_dim(const AttnArgs& a, int shape, bool f16, bool kv8, hipStrea
 
 }  // namespace
 
-AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len) {
+AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len,
+                   int64_t all_rows) {
   AttnPlan p;
   const int64_t rows = max_nodes * G;
   // 8 trees over 8000 positions (dim 128, bf16), rows of a key head: 32 rows
@@ -1328,6 +1329,11 @@ AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t m
   const int64_t units = B * Hk * p.ntiles;
   const int64_t step = p.shape == AT_STREAM16 ? 128 : 64;  // positions of one round of the waves
   const int64_t steps = (max_len + step - 1) / step;
+  // Parts of splits take 128 MB at most, so that a call's workspace is bounded.
+  // (With 32 heads of 128: 2100 nodes over 5000 positions take 390 us in nine
+  // splits of 35 MB and 322 in three; 3 x 1400 over 2000 432 and 289; 4200 over
+  // 12000 1254 in four of 70 MB, and 1353 whole.)
+  const int64_t most = std::max<int64_t>(1, ((int64_t)1 << 27) / (all_rows * (D + 2) * (int64_t)sizeof(float)));
   int64_t ns;
   if (p.shape == AT_STREAM16) {
     // A workgroup for each CU; more make more parts to join (one sequence of
@@ -1336,13 +1342,13 @@ AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t m
     // sequences of up to 8191, 8-bit: 143 us with 768, 127 with 1536).
     ns = (256 + units - 1) / units;
     if (units * ns < 1536) ns = std::max(ns, std::min((1536 + units - 1) / units, (max_len + 2047) / 2048));
-    ns = std::min(ns, steps);
+    ns = std::min({ns, steps, most});
   } else {
     // as many as fill whole rounds best; splits of four tiles at least
     const int64_t slots = 256;
     double best = 0;
     ns = 1;
-    for (int64_t n = 1; n <= std::min<int64_t>(16, (steps + 3) / 4); ++n) {
+    for (int64_t n = 1; n <= std::min({(int64_t)16, (steps + 3) / 4, most}); ++n) {
       const int64_t rounds = (units * n + slots - 1) / slots;
       const double use = (double)(units * n) / (double)(rounds * slots) - 0.01 * (double)n;
       if (use > best + 1e-9) { best = use; ns = n; }

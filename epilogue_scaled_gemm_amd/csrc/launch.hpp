@@ -198,7 +198,9 @@ struct AttnPlan {
   bool arrival;  // the last workgroup joins the splits (else a second launch)
   int64_t ntiles, nsplit, chunk;
 };
-AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len);
+// all_rows: of all heads and sequences.
+AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len,
+                   int64_t all_rows);
 // D is 64, 128 or 256.
 hipError_t launch_attention(const AttnArgs& a, int D, int shape, bool f16, bool kv8, hipStream_t s);
 

@@ -400,8 +400,8 @@ typedef struct {
  * rounded to dtype for the product with the values (fp16: below 2^-25 of the
  * row's largest with fewer bits).  Positions beyond the
  * page table are cut off.  Long contexts are split over workgroups, whose
- * sums go to the handle's workspace (grown on demand: warm a shape up before
- * capturing it).  Up to 2^25 rows (tokens * q_heads); page strides below 2^30
+ * sums go to the handle's workspace (grown on demand, by 128 MB at most: warm a
+ * shape up before capturing it).  Up to 2^25 rows (tokens * q_heads); page strides below 2^30
  * and, times page_size, in-page strides too (a cache may be larger). */
 int lin_gemm_tree_attention(lin_gemm_t h, const lin_attention_t *args, void *stream);
 
