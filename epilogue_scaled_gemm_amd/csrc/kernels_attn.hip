@@ -242,6 +242,13 @@ template <bool F16> __device__ inline float row_lse(float m, float l) {
   return (m + (__builtin_amdgcn_logf(l) - LIFT<F16>)) * 0.69314718056f;
 }
 
+// x, as a value of its own: what is computed from it is not kept in registers
+// over a loop that has better use for them.
+__device__ inline int again(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // ------------------------------------------------- rows with far scores
 // A row's exponents are s sc - M with M = m sc, rounded: all of them are off by
 // what M was rounded by, which cancels as long as it is small.  Where M gets to
@@ -465,8 +472,10 @@ template <int D, bool KV8> constexpr int stream_lds_bytes() {
          4 * 16 * 8;
 }
 
+// (Dim 128 over codes just fits three workgroups on a CU: 200 x 1000 positions take
+// 86 us, and 96 with two.)
 template <int D, bool F16, bool KV8>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 && KV8 ? 3 : 2) void stream_kernel(AttnArgs a) {
   constexpr int ES = KV8 ? 1 : 2;
   constexpr int RB = D * ES;           // bytes of a cache row
   constexpr int KS = D / 32;           // steps of the first product
@@ -712,14 +721,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void stream_kernel(AttnArgs 
     if (wave == 0) {
       uint64_t rows = __ballot(live && is_far(m)) & 0xFFFF;
       while (__builtin_expect(rows != 0, 0)) {
-        const int r = __builtin_ctzll(rows), row = row0 + r;
+        const int r = __builtin_ctzll(rows), row = row0 + r, ln = again(lane);
         float* const buf = (float*)smem;
         far_row<D, F16, KV8>(a, j, cache, a.q + (int64_t)(j.t0 + row / a.G) * a.q_ts +
-                             (int64_t)(j.hk * a.G + row % a.G) * a.q_hs, row / a.G, lo, hi, buf, lane);
+                             (int64_t)(j.hk * a.G + row % a.G) * a.q_hs, row / a.G, lo, hi, buf, ln);
         wave_sync();
-        if (col == r) {
+        if ((ln & 15) == r) {
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt) o[dt] = *(const f32x4*)(buf + dt * 16 + grp * 4);
+          for (int dt = 0; dt < DT; ++dt) o[dt] = *(const f32x4*)(buf + dt * 16 + (ln >> 4) * 4);
           m = buf[D];
           l = buf[D + 1];
         }
@@ -830,13 +839,6 @@ template <int D> __device__ inline i32x4 value_frag(const char* sv, int r0, int 
 __device__ inline void clear(f32x16& p) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) p[i] = 0.f;
-}
-
-// x, as a value of its own: what is computed from it is not kept in registers
-// over a loop that has better use for them.
-__device__ inline int again(int x) {
-  asm volatile("" : "+v"(x));
-  return x;
 }
 
 // One wave's 32 rows: what the tile kernels keep of them.
