@@ -23,9 +23,9 @@
 //    the cache): every wave runs through positions of its own, 32 at a time,
 //    without barriers: keys go from memory straight into MFMA operands,
 //    values through the wave's own LDS.
-//  - tile_kernel (many rows: large trees, parts of prompts; bound by issue
-//    and the matrix units): 32 rows per wave, all waves share each tile of
-//    positions in LDS, loaded up to three tiles ahead.
+//  - tile_kernel (many rows: large trees, parts of prompts; bound by a wait
+//    for its loads in every step, see there): 32 rows per wave, all waves
+//    share each tile of positions in LDS.
 // Long contexts are split over workgroups; those write (m, l, O) in 32 bits,
 // and join_kernel, or of few workgroups the last to arrive, joins them.
 #include <type_traits>
@@ -458,11 +458,11 @@ __global__ __launch_bounds__(256) void join_kernel(AttnArgs a, int bm, int per) 
 // the transposing reads of V take the same eight.
 //
 // Bound by reading the cache: 48 sequences of up to 8191 positions, 8 key
-// heads of 128 values, four query heads each, in 8-bit codes take 127 us
-// (4.8 TB/s) and in bf16 223 us (5.5 TB/s; a large read reaches 5.4 to 5.9).
+// heads of 128 values, four query heads each, in 8-bit codes take 124 us
+// (5.0 TB/s) and in bf16 223 us (5.5 TB/s; a large read reaches 5.4 to 5.9).
 // Four waves without a barrier keep loads of 32 KB each on their way; with a
 // shared tile of 128 rows, of which 16 are used, the 8-bit call takes 231 us,
-// 200 x 1000 positions 297 instead of 84.  Short calls are a chain of
+// 200 x 1000 positions 297 instead of 85.  Short calls are a chain of
 // latencies (page, keys, scores, values, join): 10 us for one token over 1024.
 template <int D, bool KV8> constexpr int stream_tile_bytes() { return 32 * D * (KV8 ? 1 : 2); }
 template <int D, bool KV8> constexpr int stream_lds_bytes() {
@@ -1002,21 +1002,31 @@ template <int D> constexpr int tile_lds_bytes() { return TILE_BUFS * tile_positi
 // priority, which keeps the two waves of a SIMD out of step: one's products
 // run under the other's exponentials.
 //
-// Bound by issue: a wave needs about 400 instructions per tile for its 32
-// MFMAs, and two waves per SIMD (what 250 registers allow) do not hide each
-// other fully.  Four trees of 64 nodes with four heads to a key head over
-// 32000 positions (dim 128, bf16): 175 us in this kernel, of which the tiles'
-// way into LDS alone takes 103 (5.1 TB/s) and the arithmetic alone 143 (0.94
-// PFLOP/s); 1500 nodes over 5001: 0.86 PFLOP/s.
+// What bounds the 16-bit forms: of the three tiles ahead the compiled loop keeps
+// none.  The compiler takes the transposing reads of the values for reads of
+// what the direct loads still write, and waits for all loads before those of
+// each block of 32 positions; and the page numbers, which are loaded after the
+// newest tile and used at the next step's start, are waited for there, with
+// everything issued before them.  So each tile's way from memory is covered by
+// half a softmax only, the counted waits in `finish` never bind, and the matrix
+// units are busy 36% of the time.  Open: reads that carry no such dependence, and
+// page numbers that are loaded earlier.
+//   Four trees of 64 nodes with four heads to a key head over 32000 positions
+// (dim 128, bf16): 181 us in this kernel, of which the tiles' way into LDS alone
+// takes 103 (5.1 TB/s) and the arithmetic alone 143 (0.94 PFLOP/s); 1500 nodes over
+// 5001: 0.84 PFLOP/s.  Over e4m3 codes 171 us and 0.85 PFLOP/s: nothing waits for
+// LDS there, but widening costs registers (dim 128 spills 3 to 5 of 256, dim 256
+// 8 or 9 of 512).
 // Dim 256 has four waves, one per SIMD: O and Q of 32 rows take 200 registers.
-// 16 trees of 64 nodes over 2000 positions: 175 us (0.38 PFLOP/s: nothing runs
+// 16 trees of 64 nodes over 2000 positions: 168 us (0.40 PFLOP/s: nothing runs
 // beside a wave's exponentials), and 25 more with the LDS offsets of the
 // fragments kept over the loop, for which O went to memory.
-// Measured and not kept:
-// strict alternation of the two waves between barriers (215 us), the first
-// product of the next block inside the softmax of this one (spills), fragments
-// of the values read before the softmax (spills), page numbers by scalar loads
-// (their counter is the LDS reads' too: 195 us).
+// Measured and not kept, all with the waits described above, so that other
+// results are possible without them: strict alternation of the two waves
+// between barriers (215 us), the first product of the next block inside the
+// softmax of this one (spills), fragments of the values read before the
+// softmax (spills), page numbers by scalar loads (their counter is the LDS
+// reads' too: 195 us).
 template <int D, int CW, bool F16, bool KV8>
 __global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(AttnArgs a) {
   constexpr int THREADS = 64 * tile_waves<D>();
@@ -1320,6 +1330,8 @@ AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t m
                    int64_t all_rows) {
   AttnPlan p;
   const int64_t rows = max_nodes * G;
+  // (Measured at dim 128 over 16-bit caches of thousands of positions; the other
+  // dims, codes and short contexts follow the same borders unmeasured.)
   // 8 trees over 8000 positions (dim 128, bf16), rows of a key head: 32 rows
   // take 67 us in tiles of 128 and 83 in two tiles of the streaming kernel, 128
   // rows 82 and (tiles of 256) 88, 192 rows 118 and 101.  16 rows stream: 48

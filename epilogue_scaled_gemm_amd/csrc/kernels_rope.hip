@@ -13,9 +13,9 @@
 // Memory bound: 2 bytes in and out per value.  A head is D / 8 lanes of 16
 // bytes, so its norm is a reduction by lane shuffles and the partner of a
 // half-split pair is another lane of the same group; nothing goes through
-// LDS.  8191 tokens of 40 heads of 128 values (bf16) take 43 us (3.9 TB/s; a
+// LDS.  8191 tokens of 40 heads of 128 values (bf16) take 44 us (3.9 TB/s; a
 // large copy reaches 4.8), 4099 tokens of 32 query and 8 key heads with their
-// values stored to pages 25 us (3.9 TB/s).  A decode step is one chain of
+// values stored to pages 26 us (3.9 TB/s).  A decode step is one chain of
 // latencies: 4 us in the kernel, 8 to 11 with the call around it.
 #include "launch.hpp"
 

@@ -233,7 +233,7 @@ __global__ __launch_bounds__(SC_THREADS, ET == 2 ? 6 : 8) void score_kernel(Scor
   __shared__ uint64_t found[SC_WAVES][FOUND];
   __shared__ __align__(16) float tops[SCORE_BATCHES * SC_WAVES * 4];  // of 16 lanes each
   __shared__ Sums sums[SC_WAVES];
-  __shared__ int counts[SC_WAVES], arrival;
+  __shared__ int counts[SC_WAVES];
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
