@@ -544,6 +544,21 @@ def load_traffic(kernel, digest):
     return k.get("bytes_per_launch")
 
 
+# What the JSON line keeps of a row of the shape table (whole rows go to stderr,
+# as "[shape]" lines) and of the read ceiling: readers keep a limited tail of the
+# output, and with everything in it the line had grown to 23,000 characters.
+SHAPE_KEYS = ("shape", "M", "N", "K", "us", "roof_frac", "of_stream_ceiling")
+CEILING_KEYS = ("MiB", "us", "TBps", "hbm_frac")
+
+
+def json_line(out):
+    """The benchmark's one line of output."""
+    def short(rows, keys):
+        return None if rows is None else [{k: r[k] for k in keys if k in r} for r in rows]
+    return json.dumps(dict(out, shapes=short(out["shapes"], SHAPE_KEYS),
+                           hbm_stream_ceiling=short(out["hbm_stream_ceiling"], CEILING_KEYS)))
+
+
 def main():
     args = parse()
     world = int(os.environ.get("WORLD_SIZE", "1"))
@@ -708,7 +723,7 @@ def main():
         "shapes": shapes,
         "source_digest": digest,
     }
-    print(json.dumps(out), flush=True)
+    print(json_line(out), flush=True)
     h.close()
 
 
