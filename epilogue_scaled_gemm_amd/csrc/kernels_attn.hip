@@ -766,7 +766,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 && KV8 ? 3 : 2) void s
         if (grp == 0) st_agent((double*)(a.part_ml + pr * 2), __builtin_bit_cast(double, make_float2(m, l)));
       }
     }
-    if (nsp == 1 || !a.counters) continue;  // (the last barrier is past smem's last use)
+    // (past the last barrier smem has had no use but far_row's, in wave 0's own part)
+    if (nsp == 1 || !a.counters) continue;
 
     // Arrival: the workgroup that comes last joins the splits.  Partials are
     // written and read with agent-scope atomics, which are coherent across the
