@@ -338,6 +338,126 @@ int run_score(lin_gemm_t h, const lin_score_t* p, hipStream_t s) {
   return e == hipSuccess ? LIN_OK : hip_fail(h, e, "log-probability launch");
 }
 
+int run_norm(lin_gemm_t h, const lin_norm_t* p, hipStream_t s) {
+  if (!p) return fail(h, LIN_ERR_INVALID_ARG, "null arguments");
+  if (p->dtype != LIN_Q_BF16 && p->dtype != LIN_Q_FP16)
+    return fail(h, LIN_ERR_INVALID_ARG, "dtype must be LIN_Q_BF16 or LIN_Q_FP16");
+  if (p->rows < 0 || p->width < 0) return fail(h, LIN_ERR_INVALID_ARG, "negative size");
+  if (p->codes && (p->kind < LIN_DQ_FP8_TOKEN || p->kind > LIN_DQ_FP8_BLOCK))
+    return fail(h, LIN_ERR_INVALID_ARG, "unknown quantization kind " + std::to_string(p->kind));
+  if (!(p->eps >= 0) || !std::isfinite((float)p->eps))
+    return fail(h, LIN_ERR_INVALID_ARG, "eps must be finite, in binary32 too, and not negative");
+  const int64_t step = !p->codes ? 8 : p->kind == LIN_DQ_FP8_BLOCK ? 128 : 16;
+  if (p->width < 1 || p->width > lg::NORM_MAX_WIDTH || p->width % step != 0)
+    return fail(h, LIN_ERR_UNSUPPORTED, "width must be a multiple of " + std::to_string(step) + " up to 32768");
+  if (p->rows > ((int64_t)1 << 31)) return fail(h, LIN_ERR_UNSUPPORTED, "more than 2^31 rows");
+  if (p->rows == 0) return LIN_OK;
+  if (!p->residual_out && !p->out && !p->codes)
+    return fail(h, LIN_ERR_INVALID_ARG, "no output is asked for");
+  if (!p->x || !p->weight || (p->codes && !p->scales))
+    return fail(h, LIN_ERR_INVALID_ARG, "null x, weight or scales");
+  const struct { const void* at; int64_t stride; } rows[] = {{p->x, p->x_stride}, {p->residual, p->residual_stride},
+      {p->residual_out, p->residual_out_stride}, {p->out, p->out_stride}};
+  for (const auto& r : rows) {
+    if (!r.at) continue;
+    if (p->rows > 1 && r.stride < p->width) return fail(h, LIN_ERR_INVALID_ARG, "a row stride below width");
+    if (misaligned(r.at) || (p->rows > 1 && r.stride % 8 != 0))
+      return fail(h, LIN_ERR_UNSUPPORTED, "rows must be multiples of 16 bytes apart");
+  }
+  if (misaligned(p->weight) || misaligned(p->codes) || bad4(p->scales))
+    return fail(h, LIN_ERR_UNSUPPORTED, "weight and codes must be 16-byte aligned, scales 4-byte aligned");
+  lg::NormArgs a{};
+  a.x = (const uint16_t*)p->x;
+  a.res = (const uint16_t*)p->residual;
+  a.w = (const uint16_t*)p->weight;
+  a.res_out = (uint16_t*)p->residual_out;
+  a.out = (uint16_t*)p->out;
+  a.codes = (uint8_t*)p->codes;
+  a.scales = p->scales;
+  a.T = p->rows;
+  a.x_s = p->x_stride;
+  a.res_s = p->residual_stride;
+  a.res_out_s = p->residual_out_stride;
+  a.out_s = p->out_stride;
+  a.N = (int)p->width;
+  a.eps = (float)p->eps;
+  hipError_t e = lg::launch_norm(a, p->codes ? (int)p->kind : -1, p->dtype == LIN_Q_FP16, s);
+  return e == hipSuccess ? LIN_OK : hip_fail(h, e, "norm launch");
+}
+
+int run_lora(lin_gemm_t h, const lin_lora_t* p, hipStream_t s) {
+  if (!p) return fail(h, LIN_ERR_INVALID_ARG, "null arguments");
+  if (p->dtype != LIN_Q_BF16 && p->dtype != LIN_Q_FP16)
+    return fail(h, LIN_ERR_INVALID_ARG, "dtype must be LIN_Q_BF16 or LIN_Q_FP16");
+  if (p->rows < 0 || p->inner < 0 || p->width < 0 || p->adapters < 0)
+    return fail(h, LIN_ERR_INVALID_ARG, "negative size");
+  if (p->rank < 8 || p->rank > lg::LORA_MAX_RANK || p->rank % 8 != 0)
+    return fail(h, LIN_ERR_UNSUPPORTED, "rank must be a multiple of 8 from 8 to 128");
+  if (p->inner < 8 || p->inner % 8 != 0 || p->inner > (1 << 20))
+    return fail(h, LIN_ERR_UNSUPPORTED, "inner must be a multiple of 8 up to 2^20");
+  if (p->width < 1 || p->width > (1 << 20)) return fail(h, LIN_ERR_UNSUPPORTED, "width must be in 1 .. 2^20");
+  if (p->rows > kMaxTokens || p->adapters > ((int64_t)1 << 30))
+    return fail(h, LIN_ERR_UNSUPPORTED, "more than 2^23 rows or 2^30 adapters");
+  if (p->slices < 1 || p->slices > lg::LORA_MAX_SLICES)
+    return fail(h, LIN_ERR_UNSUPPORTED, "slices must be in 1 .. 4");
+  int64_t sum = 0;
+  for (int i = 0; i < p->slices; ++i) {
+    if (p->slice_width[i] < 1 || p->slice_width[i] > p->width)
+      return fail(h, LIN_ERR_INVALID_ARG, "a slice needs columns, and no more than width");
+    sum += p->slice_width[i];
+  }
+  if (sum != p->width) return fail(h, LIN_ERR_INVALID_ARG, "the slices must add up to width");
+  if (p->rows == 0) return LIN_OK;
+  if (!p->x || !p->ids || !p->out || (p->adapters > 0 && (!p->a || !p->b)))
+    return fail(h, LIN_ERR_INVALID_ARG, "null x, a, b, ids or out");
+  if (p->rows > 1 && (p->x_stride < p->inner || p->out_stride < p->width || (p->base && p->base_stride < p->width)))
+    return fail(h, LIN_ERR_INVALID_ARG, "a row stride below the row");
+  if (misaligned(p->x) || misaligned(p->a) || misaligned(p->b) || (p->rows > 1 && p->x_stride % 8 != 0))
+    return fail(h, LIN_ERR_UNSUPPORTED, "x, its rows, a and b must be multiples of 16 bytes");
+  if (bad4(p->ids) || bad4(p->factors) || ((reinterpret_cast<uintptr_t>(p->base) | reinterpret_cast<uintptr_t>(p->out)) & 1))
+    return fail(h, LIN_ERR_UNSUPPORTED, "operands must be aligned to their elements");
+  lg::LoraArgs a{};
+  a.a = (const uint16_t*)p->a;
+  a.b = (const uint16_t*)p->b;
+  a.factors = p->factors;
+  a.x_s = p->x_stride;
+  a.base_s = p->base_stride;
+  a.out_s = p->out_stride;
+  a.n = (int)p->adapters;
+  a.K = (int)p->inner;
+  a.N = (int)p->width;
+  a.R = (int)p->rank;
+  a.S = (int)p->slices;
+  a.SR = a.R * a.S;
+  a.vec = !misaligned(p->out) && !misaligned(p->base);
+  if (p->rows > 1) a.vec = a.vec && p->out_stride % 8 == 0 && (!p->base || p->base_stride % 8 == 0);
+  for (int i = 0; i < a.S; ++i) {
+    a.width[i] = (int)p->slice_width[i];
+    if (i + 1 < a.S) a.vec = a.vec && a.width[i] % 8 == 0;
+  }
+  // h takes 128 MB at most: further rows follow in launches of their own.
+  const int64_t room = (int64_t)1 << 25;  // values
+  const int64_t most = room / a.SR / 64 * 64;
+  for (int64_t t0 = 0; t0 < p->rows; t0 += most) {
+    a.T = std::min(p->rows - t0, most);
+    a.x = (const uint16_t*)p->x + t0 * a.x_s;
+    a.base = p->base ? (const uint16_t*)p->base + t0 * a.base_s : nullptr;
+    a.out = (uint16_t*)p->out + t0 * a.out_s;
+    a.ids = p->ids + t0;
+    lg::LoraPlan plan = lg::lora_plan(a.T, a.K, a.width, a.S, a.SR, a.n);
+    plan.ksplit = std::max<int64_t>(1, std::min(plan.ksplit, room / (a.T * a.SR)));
+    a.slots = (int)plan.slots;
+    a.ksplit = (int)plan.ksplit;
+    a.blocks = (int)plan.blocks;
+    int rc = ensure_bytes(h, (size_t)a.ksplit * (size_t)a.T * (size_t)a.SR * sizeof(float), s);
+    if (rc != LIN_OK) return rc;
+    a.h = (float*)h->ws;
+    hipError_t e = lg::launch_lora(a, plan, p->dtype == LIN_Q_FP16, s);
+    if (e != hipSuccess) return hip_fail(h, e, "adapter launch");
+  }
+  return LIN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -356,6 +476,14 @@ int lin_gemm_tree_attention(lin_gemm_t h, const lin_attention_t* args, void* str
 
 int lin_gemm_token_logprobs(lin_gemm_t h, const lin_score_t* args, void* stream) {
   return guarded(h, [&] { return run_score(h, args, (hipStream_t)stream); });
+}
+
+int lin_gemm_add_rms_norm(lin_gemm_t h, const lin_norm_t* args, void* stream) {
+  return guarded(h, [&] { return run_norm(h, args, (hipStream_t)stream); });
+}
+
+int lin_gemm_lora_add(lin_gemm_t h, const lin_lora_t* args, void* stream) {
+  return guarded(h, [&] { return run_lora(h, args, (hipStream_t)stream); });
 }
 
 }  // extern "C"

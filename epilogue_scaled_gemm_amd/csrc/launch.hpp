@@ -224,4 +224,42 @@ constexpr int SCORE_BATCHES = 64;  // of a wave in one slice, at most
 void score_plan(int64_t T, int64_t V, int elem, int* nsplit, int64_t* slice);
 hipError_t launch_score(const ScoreArgs& a, int elem, hipStream_t s);
 
+// Norm of the stream with the residual's addition and 8-bit codes
+// (kernels_norm.hip).  Strides of rows, in elements; N a multiple of 8 (16 with
+// codes per token, 128 with codes per block), at most NORM_MAX_WIDTH.
+struct NormArgs {
+  const uint16_t *x, *res, *w;   // res may be null
+  uint16_t *res_out, *out;       // either may be null
+  uint8_t* codes;                // [T][N]
+  float* scales;                 // [T] or [T][N/128]
+  int64_t T, x_s, res_s, res_out_s, out_s;
+  int N;
+  float eps;
+};
+constexpr int NORM_MAX_WIDTH = 32768;
+// kind: DQKind, or -1 for no codes.
+hipError_t launch_norm(const NormArgs& a, int kind, bool f16, hipStream_t s);
+
+// Low-rank adapters beside a shared projection (kernels_lora.hip).
+constexpr int LORA_MAX_SLICES = 4, LORA_MAX_RANK = 128;
+struct LoraArgs {
+  const uint16_t *x, *a, *b, *base;  // [T][K], [n][SR][K], [n][N][R], [T][N] or null
+  uint16_t* out;                     // [T][N], may be base
+  const int* ids;                    // [T]; outside [0, n): no adapter
+  const float* factors;              // [n] or null
+  float* h;                          // [ksplit][T][SR]
+  int64_t T, x_s, base_s, out_s;
+  int n, K, N, R, S, SR;
+  int width[LORA_MAX_SLICES];        // columns of each slice
+  int vec;                           // rows of base and out and their slices are 16-byte aligned
+  int slots, ksplit, blocks;
+};
+// slots: workgroups over a window's adapters; tiles of 16 rows of A per workgroup;
+// ksplit parts of k; blocks of 64 columns per workgroup.
+struct LoraPlan {
+  int64_t slots, tiles, ksplit, blocks;
+};
+LoraPlan lora_plan(int64_t T, int64_t K, const int* width, int S, int SR, int64_t n);
+hipError_t launch_lora(const LoraArgs& a, const LoraPlan& p, bool f16, hipStream_t s);
+
 }  // namespace lg

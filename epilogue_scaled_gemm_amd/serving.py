@@ -29,16 +29,21 @@ import torch
 _HEADS = struct.Struct("<36qd5q")
 _ATTENTION = struct.Struct("<31qd2q")
 _SCORE = struct.Struct("<6qd5q")
+_NORM = struct.Struct("<10qd5q")
+_LORA = struct.Struct("<21q")
 _DTYPE16 = {torch.bfloat16: 0, torch.float16: 1}
 _SCORE_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _NO = (0, 0, 0)
+_NORM_KIND = {"fp8_token": (0, torch.float8_e4m3fn), "int8_token": (1, torch.int8),
+              "fp8_block": (2, torch.float8_e4m3fn)}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def declare(lib):
     """Argument types of the serving entry points."""
-    for name in ("qk_norm_rope", "kv_append", "tree_attention", "token_logprobs"):
+    for name in ("qk_norm_rope", "kv_append", "tree_attention", "token_logprobs", "add_rms_norm",
+                 "lora_add"):
         f = getattr(lib, "lin_gemm_" + name)
         f.argtypes = [ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p]
         f.restype = ctypes.c_int
@@ -87,6 +92,19 @@ def _flat(name, t, count, dtype):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return _at(name, t)
+
+
+def _rows(name, t, shape, dtype):
+    """(address, row stride) of a [rows, width] view, (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} (no broadcasting), got {list(t.shape)}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the values of a row must be contiguous")
+    return _at(name, t), t.stride(0) if shape[0] > 1 else 0
 
 
 def _cache_type(k_cache, dtype, k_scale, v_scale):
@@ -276,6 +294,71 @@ class ServingOps:
         if rc:
             self._check(rc, "lin_gemm_token_logprobs")
         return logprobs
+
+    def add_rms_norm(self, x, weight, residual=None, residual_out=None, out=None, codes=None,
+                     scales=None, kind="fp8_token", eps=1e-6, stream=None):
+        """Norm of s = x + residual (x alone without one) over rows [T, N]:
+        residual_out = s, out = s / sqrt(mean(s^2) + eps) * weight, and the
+        codes [T, N] of the unrounded out with their scales, as in quantize
+        (kind "fp8_token" or "int8_token": scales [T]; "fp8_block": scales
+        [T, N / 128]).  Outputs that are None are not computed; one at
+        least is asked for.  residual_out and out may be x or the residual
+        themselves.  Returns (residual_out, out, codes, scales)."""
+        _forward_only(x, weight, residual)
+        dtype = x.dtype
+        if dtype not in _DTYPE16 or x.dim() != 2:
+            raise ValueError("x must be [rows, width] in bfloat16 or float16")
+        T, N = shape = x.shape
+        if kind not in _NORM_KIND:
+            raise ValueError(f"kind must be one of {sorted(_NORM_KIND)}, got {kind!r}")
+        code, cdt = _NORM_KIND[kind]
+        if (codes is None) != (scales is None):
+            raise ValueError("codes need scales, and scales codes")
+        args = _NORM.pack(
+            _DTYPE16[dtype], T, N, *_rows("x", x, shape, dtype),
+            *_rows("residual", residual, shape, dtype),
+            *_rows("residual_out", residual_out, shape, dtype),
+            _flat("weight", weight, N, dtype), float(eps), *_rows("out", out, shape, dtype), code,
+            _flat("codes", codes, T * N, cdt),
+            _flat("scales", scales, T * (N // 128) if code == 2 else T, torch.float32))
+        rc = self._lib.lin_gemm_add_rms_norm(self._h, args, _stream_of(stream, x))
+        if rc:
+            self._check(rc, "lin_gemm_add_rms_norm")
+        return residual_out, out, codes, scales
+
+    def lora_add(self, x, a, b, ids, out, base=None, factors=None, slices=None, stream=None):
+        """Low-rank adapters beside a shared projection: out [T, N] = base +
+        factors[i] (x a[i]^T) b[i]^T with i = ids[t].
+
+        x [T, K], a [adapters, rank, K], b [adapters, N, rank], ids int32
+        [T] (outside [0, adapters): the row has no adapter), factors fp32
+        [adapters] (1 without).  base is the shared projection's output [T,
+        N], or None for 0; out may be base.  slices: the widths of up to
+        four parts of the N columns that have adapters of their own, as in
+        a QKV product; a is then [adapters, slices * rank, K], the first
+        rank rows for the first part.  Returns out."""
+        _forward_only(x, a, b, base, factors)
+        dtype = x.dtype
+        if dtype not in _DTYPE16 or x.dim() != 2 or a.dim() != 3 or b.dim() != 3 or out.dim() != 2:
+            raise ValueError("x must be [rows, inner] in bfloat16 or float16, a [adapters, slices * "
+                             "rank, inner], b [adapters, width, rank], out [rows, width]")
+        T, K = x.shape
+        n, N, R = b.shape
+        widths = (N,) if slices is None else tuple(int(w) for w in slices)
+        if not 1 <= len(widths) <= 4 or sum(widths) != N:
+            raise ValueError(f"slices must be up to four widths that add up to {N}, got {slices}")
+        if a.shape != (n, len(widths) * R, K):
+            raise ValueError(f"a must be {[n, len(widths) * R, K]}, got {list(a.shape)}")
+        args = _LORA.pack(
+            _DTYPE16[dtype], T, K, N, R, *_rows("x", x, x.shape, dtype), n,
+            _flat("a", a, a.numel(), dtype), _flat("b", b, b.numel(), dtype),
+            _flat("ids", ids, T, torch.int32), _flat("factors", factors, n, torch.float32),
+            *_rows("base", base, (T, N), dtype), *_rows("out", out, (T, N), dtype), len(widths),
+            *(widths + (0, 0, 0))[:4])
+        rc = self._lib.lin_gemm_lora_add(self._h, args, _stream_of(stream, x))
+        if rc:
+            self._check(rc, "lin_gemm_lora_add")
+        return out
 
 
 # ------------------------------------------------------------------- plans

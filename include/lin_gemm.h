@@ -428,6 +428,79 @@ typedef struct {
  * some indices in range).  Rows need no alignment beyond their element's. */
 int lin_gemm_token_logprobs(lin_gemm_t h, const lin_score_t *args, void *stream);
 
+/* ------------------------------------------------ around the linear layers
+ *
+ * Forward only, under the rules of the serving operators above. */
+typedef struct {
+    int64_t dtype;            /* LIN_Q_BF16 or LIN_Q_FP16                     */
+    int64_t rows, width;      /* width: a multiple of 8 up to 32768           */
+    const void *x;            /* [rows][width], rows x_stride elements apart  */
+    int64_t x_stride;
+    const void *residual;     /* [rows][width] or NULL                        */
+    int64_t residual_stride;
+    void *residual_out;       /* [rows][width] or NULL: x + residual; may be
+                                 the residual or x itself                     */
+    int64_t residual_out_stride;
+    const void *weight;       /* [width]                                      */
+    double eps;
+    void *out;                /* [rows][width] or NULL: the normalised rows;
+                                 may be x or the residual itself              */
+    int64_t out_stride;
+    int64_t kind;             /* enum lin_dq_kind of the codes                */
+    void *codes;              /* [rows][width] bytes, contiguous, or NULL     */
+    float *scales;            /* [rows], or [rows][width / 128] for blocks    */
+} lin_norm_t;
+
+/* Root-mean-square norm of a decoder's stream, with the residual's addition
+ * before it and the quantization that the next layer wants behind it:
+ *   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * weight
+ * computed in binary32 (rows of any finite size).  residual_out = s and out =
+ * y, rounded once; codes and scales as lin_gemm_quantize gives them, but of
+ * the unrounded y, so they go straight into lin_gemm_run (A and scales->a).
+ * At least one of residual_out, out and codes is asked for.  Addresses and
+ * row strides are multiples of 16 bytes; width is a multiple of 16 with codes
+ * per token and of 128 with codes per block.  A row with an infinity or NaN
+ * gives what the formula gives in out, unspecified codes and scales.  No
+ * allocation. */
+int lin_gemm_add_rms_norm(lin_gemm_t h, const lin_norm_t *args, void *stream);
+
+typedef struct {
+    int64_t dtype;            /* LIN_Q_BF16 or LIN_Q_FP16                     */
+    int64_t rows, inner, width;
+    int64_t rank;             /* a multiple of 8 up to 128 (pad with zeros)   */
+    const void *x;            /* [rows][inner], rows x_stride elements apart  */
+    int64_t x_stride;
+    int64_t adapters;
+    const void *a;            /* [adapters][slices * rank][inner], contiguous */
+    const void *b;            /* [adapters][width][rank], contiguous          */
+    const int32_t *ids;       /* [rows]: the row's adapter; outside
+                                 [0, adapters): none                          */
+    const float *factors;     /* [adapters] or NULL (1)                       */
+    const void *base;         /* [rows][width] or NULL (0)                    */
+    int64_t base_stride;
+    void *out;                /* [rows][width]; may be the base itself        */
+    int64_t out_stride;
+    int64_t slices;           /* 1 .. 4                                       */
+    int64_t slice_width[4];   /* output columns of each slice, adding up to
+                                 width                                        */
+} lin_lora_t;
+
+/* Low-rank adapters of many requests beside a shared projection, whose output
+ * is the base:
+ *   out[t, n] = base[t, n] + factors[i] * sum_r h[t, s rank + r] b[i, n, r]
+ *   h[t, j] = sum_k x[t, k] a[i, j, k],   i = ids[t], s the slice of column n
+ * Slices are the parts of one product that have adapters of their own (q, k
+ * and v of a QKV product).  Rows name adapters in any order; rows of one
+ * adapter that lie near each other read its weights once.  Rows without an
+ * adapter get the base.  h is binary32 and enters the second product with 16
+ * bits or more; sums are binary32, the result is rounded once.  inner is a
+ * multiple of 8, x and its stride, a and b multiples of 16 bytes; base and
+ * out need the alignment of their elements only (16-byte rows and slices
+ * are faster).  inner and width up to 2^20.  h goes to the handle's
+ * workspace (grown on demand, by 128 MB at most: warm a shape up before
+ * capturing it). */
+int lin_gemm_lora_add(lin_gemm_t h, const lin_lora_t *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
