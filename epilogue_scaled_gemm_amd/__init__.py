@@ -43,7 +43,8 @@ EXPORTS = ("lin_gemm_create", "lin_gemm_run", "lin_gemm_destroy", "lin_gemm_stre
            "lin_gemm_run_unfused", "lin_gemm_quantize", "lin_gemm_run_dynamic",
            "lin_gemm_run_grouped", "lin_gemm_run_noalloc", "lin_gemm_stream_read",
            "lin_gemm_qk_norm_rope", "lin_gemm_kv_append", "lin_gemm_tree_attention",
-           "lin_gemm_token_logprobs", "lin_gemm_add_rms_norm", "lin_gemm_lora_add")
+           "lin_gemm_token_logprobs", "lin_gemm_add_rms_norm", "lin_gemm_lora_add",
+           "lin_gemm_window_attention")
 DQ_KIND = {"fp8_token": 0, "int8_token": 1, "fp8_block": 2}
 X_DTYPE = {"bf16": 0, "fp16": 1}
 

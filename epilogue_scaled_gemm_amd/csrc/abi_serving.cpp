@@ -178,7 +178,8 @@ int ensure_counters(lin_gemm_t h, size_t n, hipStream_t s) {
   return LIN_OK;
 }
 
-int run_attention(lin_gemm_t h, const lin_attention_t* p, hipStream_t s) {
+// win: null without a window.
+int run_attention(lin_gemm_t h, const lin_attention_t* p, const lin_window_t* win, hipStream_t s) {
   if (!p) return fail(h, LIN_ERR_INVALID_ARG, "null arguments");
   if (p->dtype != LIN_Q_BF16 && p->dtype != LIN_Q_FP16)
     return fail(h, LIN_ERR_INVALID_ARG, "dtype must be LIN_Q_BF16 or LIN_Q_FP16");
@@ -195,6 +196,10 @@ int run_attention(lin_gemm_t h, const lin_attention_t* p, hipStream_t s) {
     return fail(h, LIN_ERR_UNSUPPORTED, "more than 2^25 rows of one head");
   if (!std::isfinite((float)(p->scale * kLog2e)))  // (what the kernels hold)
     return fail(h, LIN_ERR_INVALID_ARG, "scale must be finite, in binary32 too");
+  if (win && (win->window < 1 || win->sinks < 0))
+    return fail(h, LIN_ERR_INVALID_ARG, "window must be at least 1, sinks not negative");
+  if (win && win->positions && !p->mask)
+    return fail(h, LIN_ERR_INVALID_ARG, "positions are for nodes with a mask: others follow the context");
   int rc = check_cache(h, p->dtype, p->cache_type, p->pages, p->page_size, p->k_cache, p->v_cache,
                        {p->k_page_stride, p->k_head_stride, p->k_in_page_stride, p->v_page_stride,
                         p->v_head_stride, p->v_in_page_stride});
@@ -218,10 +223,12 @@ int run_attention(lin_gemm_t h, const lin_attention_t* p, hipStream_t s) {
       any_not_multiple(8, {p->q_token_stride, p->q_head_stride}))
     return fail(h, LIN_ERR_UNSUPPORTED, "q, out and strides must be multiples of 16 bytes");
   if (bad4(p->page_table) || bad4(p->context) || bad4(p->offsets) || bad4(p->lse) ||
-      bad4(p->k_scale) || bad4(p->v_scale) || (reinterpret_cast<uintptr_t>(p->mask) & 7))
+      bad4(p->k_scale) || bad4(p->v_scale) || (reinterpret_cast<uintptr_t>(p->mask) & 7) ||
+      (win && bad4(win->positions)))
     return fail(h, LIN_ERR_UNSUPPORTED, "plans must be 4-byte aligned, masks 8-byte aligned");
 
-  lg::AttnArgs a{};
+  lg::WindowArgs w{};
+  lg::AttnArgs& a = w;
   a.q = (const uint16_t*)p->q;
   a.k = p->k_cache;
   a.v = p->v_cache;
@@ -260,7 +267,13 @@ int run_attention(lin_gemm_t h, const lin_attention_t* p, hipStream_t s) {
   const int64_t nodes = std::min(std::max<int64_t>(p->max_nodes, 1), p->tokens);
   const int64_t room = p->max_pages * p->page_size;
   const int64_t len = std::min(std::min(p->max_context, room) + nodes, room);
-  const lg::AttnPlan plan = lg::attn_plan(p->sequences, a.Hk, a.G, (int)p->dim, nodes, len, a.rows);
+  if (win) {
+    w.positions = win->positions;
+    w.window = (int)std::min<int64_t>(win->window, (int64_t)1 << 30);  // (of at most 2^30 positions)
+    w.sinks = (int)std::min<int64_t>(win->sinks, (int64_t)1 << 30);
+  }
+  const lg::AttnPlan plan =
+      lg::attn_plan(p->sequences, a.Hk, a.G, (int)p->dim, nodes, len, a.rows, w.window, w.sinks, a.mask != nullptr);
   const int64_t work = p->sequences * a.Hk * plan.nsplit;
   if (work > kMaxGroups / plan.ntiles - 8)
     return fail(h, LIN_ERR_UNSUPPORTED, "too many workgroups for one launch");
@@ -280,7 +293,9 @@ int run_attention(lin_gemm_t h, const lin_attention_t* p, hipStream_t s) {
       a.counters = h->counters;
     }
   }
-  hipError_t e = lg::launch_attention(a, (int)p->dim, plan.shape, p->dtype == LIN_Q_FP16, kv8, s);
+  const bool f16 = p->dtype == LIN_Q_FP16;
+  hipError_t e = win ? lg::launch_window(w, (int)p->dim, plan.shape, f16, kv8, s)
+                     : lg::launch_attention(a, (int)p->dim, plan.shape, f16, kv8, s);
   return e == hipSuccess ? LIN_OK : hip_fail(h, e, "attention launch");
 }
 
@@ -471,7 +486,14 @@ int lin_gemm_kv_append(lin_gemm_t h, const lin_heads_t* args, void* stream) {
 }
 
 int lin_gemm_tree_attention(lin_gemm_t h, const lin_attention_t* args, void* stream) {
-  return guarded(h, [&] { return run_attention(h, args, (hipStream_t)stream); });
+  return guarded(h, [&] { return run_attention(h, args, nullptr, (hipStream_t)stream); });
+}
+
+int lin_gemm_window_attention(lin_gemm_t h, const lin_window_t* args, void* stream) {
+  return guarded(h, [&] {
+    if (!args) return fail(h, LIN_ERR_INVALID_ARG, "null arguments");
+    return run_attention(h, &args->attention, args, (hipStream_t)stream);
+  });
 }
 
 int lin_gemm_token_logprobs(lin_gemm_t h, const lin_score_t* args, void* stream) {

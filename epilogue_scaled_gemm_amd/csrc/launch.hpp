@@ -198,11 +198,19 @@ struct AttnPlan {
   bool arrival;  // the last workgroup joins the splits (else a second launch)
   int64_t ntiles, nsplit, chunk;
 };
-// all_rows: of all heads and sequences.
+// all_rows: of all heads and sequences.  window 0: none; masked: trees.
 AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len,
-                   int64_t all_rows);
+                   int64_t all_rows, int64_t window = 0, int64_t sinks = 0, bool masked = false);
 // D is 64, 128 or 256.
 hipError_t launch_attention(const AttnArgs& a, int D, int shape, bool f16, bool kv8, hipStream_t s);
+
+// With a sliding window (kernels_window.hip): a row at position p sees the cached
+// positions c < sinks and c > p - window.
+struct WindowArgs : AttnArgs {
+  const int* positions;    // [T] of the nodes of trees, or null: context + node
+  int window, sinks;       // 1 .. 2^30, 0 .. 2^30
+};
+hipError_t launch_window(const WindowArgs& a, int D, int shape, bool f16, bool kv8, hipStream_t s);
 
 struct ScoreArgs {
   const void* logits;

@@ -29,6 +29,7 @@ import torch
 _HEADS = struct.Struct("<36qd5q")
 _ATTENTION = struct.Struct("<31qd2q")
 _SCORE = struct.Struct("<6qd5q")
+_WINDOW = struct.Struct("<31qd5q")
 _NORM = struct.Struct("<10qd5q")
 _LORA = struct.Struct("<21q")
 _DTYPE16 = {torch.bfloat16: 0, torch.float16: 1}
@@ -42,8 +43,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 
 def declare(lib):
     """Argument types of the serving entry points."""
-    for name in ("qk_norm_rope", "kv_append", "tree_attention", "token_logprobs", "add_rms_norm",
-                 "lora_add"):
+    for name in ("qk_norm_rope", "kv_append", "tree_attention", "token_logprobs", "window_attention",
+                 "add_rms_norm", "lora_add"):
         f = getattr(lib, "lin_gemm_" + name)
         f.argtypes = [ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p]
         f.restype = ctypes.c_int
@@ -215,20 +216,8 @@ class ServingOps:
             self._check(rc, "lin_gemm_kv_append")
         return k_cache, v_cache
 
-    def tree_attention(self, q, k_cache, v_cache, out, page_table, context, offsets, max_context,
-                       max_nodes, mask=None, scale=None, k_scale=None, v_scale=None, lse=None,
-                       stream=None):
-        """Attention of nodes q [T, Hq, dim] over their sequences' caches.
-
-        page_table [B, pages per sequence], context [B] (cached tokens before
-        the nodes, whose own keys and values follow them in the cache),
-        offsets [B + 1].  max_context and max_nodes bound the two; they shape
-        the launch only.  mask int64 [T, words]: bit j % 64 of word j // 64
-        says that the node sees node j of its sequence (see tree_mask);
-        without one it sees itself and the nodes before it.  scale: 1 /
-        sqrt(dim) unless given.  out [T, Hq, dim] and lse [T, Hq] (fp32,
-        optional) are contiguous.  Returns out."""
-        _forward_only(q)
+    def _attention_part(self, q, k_cache, v_cache, out, page_table, context, offsets, max_context,
+                        max_nodes, mask, scale, k_scale, v_scale, lse):
         dtype = q.dtype
         if dtype not in _DTYPE16 or q.dim() != 3 or k_cache.dim() != 4 or page_table.dim() != 2:
             raise ValueError("q must be [tokens, heads, dim] in bfloat16 or float16, caches "
@@ -250,7 +239,7 @@ class ServingOps:
             if words * 64 < max_nodes:
                 raise ValueError(f"mask of {words} words for up to {max_nodes} nodes")
             mp_at = _flat("mask", mask, T * words, torch.int64)
-        args = _ATTENTION.pack(
+        return (
             _DTYPE16[dtype], T, Hq, Hk, D, *_heads("q", q, qs, dtype),
             *_cache("k_cache", k_cache, cs, cdt), *_cache("v_cache", v_cache, cs, cdt), kind, pages,
             page, _flat("k_scale", k_scale, Hk, torch.float32),
@@ -259,9 +248,52 @@ class ServingOps:
             _flat("offsets", offsets, B + 1, torch.int32), int(max_context), int(max_nodes),
             mp_at, words, 1.0 / math.sqrt(D) if scale is None else float(scale),
             _flat("out", out, T * Hq * D, dtype), _flat("lse", lse, T * Hq, torch.float32))
+
+    def tree_attention(self, q, k_cache, v_cache, out, page_table, context, offsets, max_context,
+                       max_nodes, mask=None, scale=None, k_scale=None, v_scale=None, lse=None,
+                       stream=None):
+        """Attention of nodes q [T, Hq, dim] over their sequences' caches.
+
+        page_table [B, pages per sequence], context [B] (cached tokens before
+        the nodes, whose own keys and values follow them in the cache),
+        offsets [B + 1].  max_context and max_nodes bound the two; they shape
+        the launch only.  mask int64 [T, words]: bit j % 64 of word j // 64
+        says that the node sees node j of its sequence (see tree_mask);
+        without one it sees itself and the nodes before it.  scale: 1 /
+        sqrt(dim) unless given.  out [T, Hq, dim] and lse [T, Hq] (fp32,
+        optional) are contiguous.  Returns out."""
+        _forward_only(q)
+        args = _ATTENTION.pack(*self._attention_part(
+            q, k_cache, v_cache, out, page_table, context, offsets, max_context, max_nodes, mask, scale,
+            k_scale, v_scale, lse))
         rc = self._lib.lin_gemm_tree_attention(self._h, args, _stream_of(stream, q))
         if rc:
             self._check(rc, "lin_gemm_tree_attention")
+        return out
+
+    def window_attention(self, q, k_cache, v_cache, out, page_table, context, offsets, max_context,
+                         max_nodes, window, sinks=0, mask=None, positions=None, scale=None,
+                         k_scale=None, v_scale=None, lse=None, stream=None):
+        """tree_attention of layers with a sliding window: of the cached
+        positions a node at position p sees those below `sinks` and those
+        above p - window (its own among them).  Without a mask p is context +
+        node; nodes with a mask have positions int32 [T] (context + depth,
+        see tree_mask; context + node without), see the nodes that the mask
+        names and of the context what the window leaves.  Pages that no node
+        sees may have been dropped: their table entries are not looked at
+        beyond the 128 positions around the visible ones, which may hold
+        anything.  Returns out."""
+        _forward_only(q)
+        part = self._attention_part(
+            q, k_cache, v_cache, out, page_table, context, offsets, max_context, max_nodes, mask, scale,
+            k_scale, v_scale, lse)
+        if positions is not None and mask is None:
+            raise ValueError("positions are for nodes with a mask: others follow the context")
+        args = _WINDOW.pack(*part, int(window), int(sinks),
+                            _flat("positions", positions, q.shape[0], torch.int32))
+        rc = self._lib.lin_gemm_window_attention(self._h, args, _stream_of(stream, q))
+        if rc:
+            self._check(rc, "lin_gemm_window_attention")
         return out
 
     def token_logprobs(self, logits, tokens, logprobs, entropy=None, top_ids=None,

@@ -406,6 +406,25 @@ typedef struct {
 int lin_gemm_tree_attention(lin_gemm_t h, const lin_attention_t *args, void *stream);
 
 typedef struct {
+    lin_attention_t attention;
+    int64_t window;           /* 1 or more positions, a row's own among them  */
+    int64_t sinks;            /* first positions that stay visible, 0 or more */
+    const int32_t *positions; /* [tokens] of nodes with a mask (context + depth
+                                 in the tree; clamped to the context's end and
+                                 the places of the sequence's nodes), or NULL:
+                                 context + node                               */
+} lin_window_t;
+
+/* lin_gemm_tree_attention of layers with a sliding window: the row at position p
+ * sees of the cached positions c what tree attention would let it see, and of
+ * that only c < sinks and c > p - window.  Where a mask names the nodes that a
+ * row sees, they are seen whatever the window; it applies to the context.
+ * Positions that no row sees are not read, but for those that share a block
+ * of 128 with a visible one, whose values do not reach the result: page table
+ * entries of dropped pages may hold anything. */
+int lin_gemm_window_attention(lin_gemm_t h, const lin_window_t *args, void *stream);
+
+typedef struct {
     int64_t dtype;            /* 0 bf16, 1 fp16, 2 fp32                       */
     int64_t rows, vocab;
     const void *logits;       /* [rows][vocab], row_stride elements apart     */

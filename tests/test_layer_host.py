@@ -86,8 +86,28 @@ def test_lora_add_refusals(handle, kw, status):
     assert _call(handle, "lin_gemm_lora_add", serving._LORA, LORA, LORA_OK, kw) == status
 
 
+WINDOW = ("dtype tokens q_heads kv_heads dim q q_ts q_hs kc kc_ps kc_hs kc_ts vc vc_ps vc_hs vc_ts "
+          "cache_type pages page_size k_scale v_scale sequences table table_stride max_pages context "
+          "offsets max_context max_nodes mask mask_words scale out lse window sinks positions").split()
+WINDOW_OK = dict(tokens=0, q_heads=4, kv_heads=2, dim=128, q=FAKE, q_ts=512, q_hs=128, kc=FAKE,
+                 kc_ps=4096, kc_hs=2048, kc_ts=128, vc=FAKE, vc_ps=4096, vc_hs=2048, vc_ts=128,
+                 pages=8, page_size=16, sequences=2, table=FAKE, table_stride=4, max_pages=4,
+                 context=FAKE, offsets=FAKE, max_context=32, max_nodes=2, scale=0.1, out=FAKE, window=16)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), OK), (dict(window=0), INVALID), (dict(window=-5), INVALID), (dict(sinks=-1), INVALID),
+    (dict(window=1 << 62, sinks=1 << 62), OK), (dict(positions=FAKE), INVALID),
+    (dict(positions=FAKE, mask=FAKE, mask_words=1), OK),
+    (dict(tokens=4, positions=FAKE + 2, mask=FAKE, mask_words=1), UNSUPPORTED),
+    (dict(dtype=2), INVALID), (dict(dim=96), UNSUPPORTED), (dict(tokens=4, q=0), INVALID),
+    (dict(tokens=4, mask=FAKE + 4, mask_words=1), UNSUPPORTED), (dict(tokens=4, out=FAKE + 2), UNSUPPORTED)])
+def test_window_attention_refusals(handle, kw, status):
+    assert _call(handle, "lin_gemm_window_attention", serving._WINDOW, WINDOW, WINDOW_OK, kw) == status
+
+
 def test_null_handle_and_null_arguments(handle):
-    for f in ("add_rms_norm", "lora_add"):
+    for f in ("add_rms_norm", "lora_add", "window_attention"):
         entry = getattr(lg.library(), "lin_gemm_" + f)
         assert entry(None, None, None) == INVALID and entry(handle._h, None, None) == INVALID
 
@@ -105,6 +125,11 @@ def test_records_match_the_header():
                 size = re.search(r"\[(\d+)\]", part)
                 count += int(size.group(1)) if size else 1
         assert count == len(names) and fmt.size == 8 * count
+    # the windowed record is the other attention's and three fields more
+    body = re.search(r"typedef struct \{([^}]*)\} lin_window_t;", text).group(1)
+    assert [x.split()[-1].lstrip("*") for x in body.replace(",", ";").split(";") if x.strip()] == [
+        "attention", "window", "sinks", "positions"]
+    assert serving._WINDOW.size == serving._ATTENTION.size + 24 == 8 * len(WINDOW)
 
 
 @pytest.fixture()
@@ -200,6 +225,29 @@ def test_binding_refuses_wrong_adapters(addressed, bad):
         error, match = RuntimeError, "forward only"
     with pytest.raises(error, match=match):
         addressed.lora_add(**kw)
+
+
+@pytest.mark.parametrize("bad", ["positions", "positions_dtype", "without_mask", "mask", "grad"])
+def test_binding_refuses_wrong_windows(addressed, bad):
+    i32 = dict(dtype=torch.int32)
+    kw = dict(q=_t(3, 4, 64), k_cache=_t(6, 2, 16, 64), v_cache=_t(6, 2, 16, 64), out=_t(3, 4, 64),
+              page_table=torch.zeros(2, 3, **i32), context=torch.zeros(2, **i32), offsets=torch.zeros(3, **i32),
+              max_context=10, max_nodes=2, window=8, mask=torch.zeros(3, 1, dtype=torch.int64),
+              positions=torch.zeros(3, **i32))
+    error, match = ValueError, None
+    if bad == "positions":
+        kw["positions"] = torch.zeros(2, **i32)
+    elif bad == "positions_dtype":
+        kw["positions"] = torch.zeros(3, dtype=torch.int64)
+    elif bad == "without_mask":
+        kw["mask"] = None
+    elif bad == "mask":
+        kw["mask"] = torch.zeros(2, 1, dtype=torch.int64)
+    elif bad == "grad":
+        kw["q"].requires_grad_()
+        error, match = RuntimeError, "forward only"
+    with pytest.raises(error, match=match):
+        addressed.window_attention(**kw)
 
 
 def test_a_row_that_stands_for_many_is_refused(addressed):
