@@ -9,9 +9,10 @@
 - ``torch.ops.lingemm.scaled_linear_grouped``: the mixture-of-experts form
   (lin_gemm_run_grouped): token-sorted rows, one weight per expert; and
   ``scaled_linear_grouped_dynamic`` for 16-bit activations quantized first.
-- ``torch.ops.lingemm.qk_norm_rope``, ``kv_append``, ``tree_attention`` and
-  ``token_logprobs``: the serving operators between the layers (the handle's
-  methods of ``serving``), forward only.
+- ``torch.ops.lingemm.qk_norm_rope``, ``kv_append``, ``tree_attention``,
+  ``window_attention``, ``token_logprobs``, ``add_rms_norm`` and ``lora_add``:
+  the serving operators between the layers (the handle's methods of
+  ``serving``), forward only.
 - ``fuse_linear_epilogues(gm, example_inputs)``: a torch.fx pass that
   rewrites ``linear -> activation [-> * alpha] [-> + residual]`` chains of a
   traced module, and the ``matmul(x, w) -> + bias -> activation ...`` chain
@@ -39,7 +40,7 @@ graph, run them once eagerly on the capture stream
 shape of the built-in table) capture on any stream.
 """
 import operator
-from typing import Optional, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 import torch.nn.functional as F
@@ -357,6 +358,33 @@ def _tree_attention_fake(q, k_cache, v_cache, page_table, context, offsets, max_
     return q.new_empty(q.shape), q.new_empty(q.shape[:2], dtype=torch.float32)
 
 
+@torch.library.custom_op("lingemm::window_attention", mutates_args=())
+def window_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                     page_table: torch.Tensor, context: torch.Tensor, offsets: torch.Tensor,
+                     max_context: int, max_nodes: int, window: int, sinks: int = 0,
+                     mask: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                     scale: Optional[float] = None, k_scale: Optional[torch.Tensor] = None,
+                     v_scale: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """tree_attention with a sliding window and first positions that stay
+    visible; returns (out [T, Hq, dim], lse [T, Hq] fp32)."""
+    _check_heads16("q", q)
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    handle_for(q.device).window_attention(q, k_cache, v_cache, out, page_table, context, offsets,
+                                          max_context=max_context, max_nodes=max_nodes, window=window,
+                                          sinks=sinks, mask=mask, positions=positions, scale=scale,
+                                          k_scale=k_scale, v_scale=v_scale, lse=lse)
+    return out, lse
+
+
+@window_attention.register_fake
+def _window_attention_fake(q, k_cache, v_cache, page_table, context, offsets, max_context, max_nodes,
+                           window, sinks=0, mask=None, positions=None, scale=None, k_scale=None,
+                           v_scale=None):
+    _check_heads16("q", q)
+    return q.new_empty(q.shape), q.new_empty(q.shape[:2], dtype=torch.float32)
+
+
 @torch.library.custom_op("lingemm::token_logprobs", mutates_args=())
 def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, top: int = 0,
                    temperature: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor,
@@ -384,6 +412,67 @@ def _token_logprobs_fake(logits, tokens, top=0, temperature=1.0):
     f32 = dict(dtype=torch.float32)
     return (logits.new_empty(T, **f32), logits.new_empty(T, **f32),
             logits.new_empty((T, top), dtype=torch.int32), logits.new_empty((T, top), **f32))
+
+
+_KINDS = {"fp8_token": torch.float8_e4m3fn, "int8_token": torch.int8,
+          "fp8_block": torch.float8_e4m3fn}
+
+
+def _norm_shapes(x, kind):
+    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("x must be [rows, width] in bfloat16 or float16")
+    if kind and kind not in _KINDS:
+        raise ValueError(f"kind must be one of {sorted(_KINDS)} or empty, got {kind!r}")
+    T, N = x.shape
+    return ((T, N), (T, N // 128) if kind == "fp8_block" else (T,)) if kind else ((0,), (0,))
+
+
+@torch.library.custom_op("lingemm::add_rms_norm", mutates_args=())
+def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
+                 kind: str = "", eps: float = 1e-6) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor,
+                                                             torch.Tensor]:
+    """(x + residual, its norm times weight, the norm's codes, their scales)
+    over rows [T, N]; without a residual the first, without a kind
+    ("fp8_token", "int8_token" or "fp8_block") the last two are empty."""
+    coded, scaled = _norm_shapes(x, kind)
+    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    total = torch.empty(x.shape if residual is not None else (0,), dtype=x.dtype, device=x.device)
+    codes = torch.empty(coded, dtype=_KINDS.get(kind, torch.int8), device=x.device)
+    scales = torch.empty(scaled, dtype=torch.float32, device=x.device)
+    handle_for(x.device).add_rms_norm(
+        x, weight, residual=residual, residual_out=total if residual is not None else None, out=out,
+        codes=codes if kind else None, scales=scales if kind else None, kind=kind or "fp8_token", eps=eps)
+    return total, out, codes, scales
+
+
+@add_rms_norm.register_fake
+def _add_rms_norm_fake(x, weight, residual=None, kind="", eps=1e-6):
+    coded, scaled = _norm_shapes(x, kind)
+    return (x.new_empty(x.shape if residual is not None else (0,)), x.new_empty(x.shape),
+            x.new_empty(coded, dtype=_KINDS.get(kind, torch.int8)),
+            x.new_empty(scaled, dtype=torch.float32))
+
+
+def _check_lora(x, b):
+    if x.dim() != 2 or b.dim() != 3 or x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("x must be [rows, inner] in bfloat16 or float16, b [adapters, width, rank]")
+
+
+@torch.library.custom_op("lingemm::lora_add", mutates_args=())
+def lora_add(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, ids: torch.Tensor,
+             base: Optional[torch.Tensor] = None, factors: Optional[torch.Tensor] = None,
+             slices: Optional[Sequence[int]] = None) -> torch.Tensor:
+    """base [T, N] (0 without) + factors[i] (x a[i]^T) b[i]^T with i = ids[t];
+    a new tensor."""
+    _check_lora(x, b)
+    out = torch.empty((x.shape[0], b.shape[1]), dtype=x.dtype, device=x.device)
+    return handle_for(x.device).lora_add(x, a, b, ids, out, base=base, factors=factors, slices=slices)
+
+
+@lora_add.register_fake
+def _lora_add_fake(x, a, b, ids, base=None, factors=None, slices=None):
+    _check_lora(x, b)
+    return x.new_empty((x.shape[0], b.shape[1]))
 
 
 # --------------------------------------------------------------- FX rewrite
