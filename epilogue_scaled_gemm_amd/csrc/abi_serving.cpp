@@ -444,11 +444,11 @@ int run_lora(lin_gemm_t h, const lin_lora_t* p, hipStream_t s) {
   a.R = (int)p->rank;
   a.S = (int)p->slices;
   a.SR = a.R * a.S;
-  a.vec = !misaligned(p->out) && !misaligned(p->base);
-  if (p->rows > 1) a.vec = a.vec && p->out_stride % 8 == 0 && (!p->base || p->base_stride % 8 == 0);
+  bool vec = !misaligned(p->out) && !misaligned(p->base);
+  if (p->rows > 1) vec = vec && p->out_stride % 8 == 0 && (!p->base || p->base_stride % 8 == 0);
   for (int i = 0; i < a.S; ++i) {
     a.width[i] = (int)p->slice_width[i];
-    if (i + 1 < a.S) a.vec = a.vec && a.width[i] % 8 == 0;
+    if (i + 1 < a.S) vec = vec && a.width[i] % 8 == 0;
   }
   // h takes 128 MB at most: further rows follow in launches of their own.
   const int64_t room = (int64_t)1 << 25;  // values
@@ -459,15 +459,22 @@ int run_lora(lin_gemm_t h, const lin_lora_t* p, hipStream_t s) {
     a.base = p->base ? (const uint16_t*)p->base + t0 * a.base_s : nullptr;
     a.out = (uint16_t*)p->out + t0 * a.out_s;
     a.ids = p->ids + t0;
-    lg::LoraPlan plan = lg::lora_plan(a.T, a.K, a.width, a.S, a.SR, a.n);
-    plan.ksplit = std::max<int64_t>(1, std::min(plan.ksplit, room / (a.T * a.SR)));
+    lg::LoraPlan plan = lg::lora_plan(a.T, a.K, a.width, a.S, a.R, a.n);
+    const int64_t split = std::max<int64_t>(1, room / (a.T * a.SR));
+    if (plan.ksplit > split) {
+      plan.ksteps = ((a.K + 63) / 64 + split - 1) / split;
+      plan.ksplit = split;
+    }
     a.slots = (int)plan.slots;
+    a.ksteps = (int)plan.ksteps;
     a.ksplit = (int)plan.ksplit;
     a.blocks = (int)plan.blocks;
-    int rc = ensure_bytes(h, (size_t)a.ksplit * (size_t)a.T * (size_t)a.SR * sizeof(float), s);
-    if (rc != LIN_OK) return rc;
-    a.h = (float*)h->ws;
-    hipError_t e = lg::launch_lora(a, plan, p->dtype == LIN_Q_FP16, s);
+    if (!plan.step) {
+      int rc = ensure_bytes(h, (size_t)a.ksplit * (size_t)a.T * (size_t)a.SR * sizeof(float), s);
+      if (rc != LIN_OK) return rc;
+      a.h = (float*)h->ws;
+    }
+    hipError_t e = lg::launch_lora(a, plan, p->dtype == LIN_Q_FP16, vec, s);
     if (e != hipSuccess) return hip_fail(h, e, "adapter launch");
   }
   return LIN_OK;

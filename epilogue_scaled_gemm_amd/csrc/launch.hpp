@@ -259,15 +259,17 @@ struct LoraArgs {
   int64_t T, x_s, base_s, out_s;
   int n, K, N, R, S, SR;
   int width[LORA_MAX_SLICES];        // columns of each slice
-  int vec;                           // rows of base and out and their slices are 16-byte aligned
-  int slots, ksplit, blocks;
+  int slots, ksteps, ksplit, blocks;
 };
-// slots: workgroups over a window's adapters; tiles of 16 rows of A per workgroup;
-// ksplit parts of k; blocks of 64 columns per workgroup.
+// step: both products in one launch (no h); slots: workgroups over a window's
+// adapters; tiles of 16 rows of A per workgroup; ksplit parts of ksteps steps of
+// 64 values of k; blocks of 64 columns per workgroup.
 struct LoraPlan {
-  int64_t slots, tiles, ksplit, blocks;
+  bool step;
+  int64_t slots, tiles, ksteps, ksplit, blocks;
 };
-LoraPlan lora_plan(int64_t T, int64_t K, const int* width, int S, int SR, int64_t n);
-hipError_t launch_lora(const LoraArgs& a, const LoraPlan& p, bool f16, hipStream_t s);
+LoraPlan lora_plan(int64_t T, int64_t K, const int* width, int S, int R, int64_t n);
+// vec: rows of base and out and their slices are 16-byte aligned.
+hipError_t launch_lora(const LoraArgs& a, const LoraPlan& p, bool f16, bool vec, hipStream_t s);
 
 }  // namespace lg
