@@ -219,6 +219,11 @@ template <> struct Span<true> {
   __device__ inline int shift(int at) const { return at >= seam ? gap : 0; }
 };
 
+template <typename Args> __device__ inline int in_sinks(const Args& a) {
+  if constexpr (WINDOWED<Args>) return a.sinks;
+  else return 0;
+}
+
 // Where the window of a node begins.  The positions of a tree's nodes are
 // clamped to those that its nodes can have.
 template <typename Args> __device__ inline int window_low(const Args& a, const Job& j, int node) {
@@ -949,11 +954,20 @@ template <int D, bool F16> struct Rows {
                                                const Job& j, int node, const int64_t* mrow, int pos,
                                                int hi, int low, int lane) {
     if constexpr (TAIL) {
+      if (WINDOWED<Args> && !a.mask && pos >= in_sinks(a)) {
+        // one range of positions: a comparison each
+        const int first = low - pos - 4 * (lane >> 5);
+        const uint32_t count = max(min(j.pos0 + node + 1, hi) - low, 0);
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const uint32_t vis = sees4(a, j, node, mrow, pos + 8 * b + 4 * (lane >> 5), hi, low);
+        for (int i = 0; i < 16; ++i)
+          p[i] = (uint32_t)(8 * (i >> 2) + (i & 3) - first) < count ? p[i] : NEG_INF;
+      } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[b * 4 + i] = (vis >> i) & 1 ? p[b * 4 + i] : NEG_INF;
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t vis = sees4(a, j, node, mrow, pos + 8 * b + 4 * (lane >> 5), hi, low);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[b * 4 + i] = (vis >> i) & 1 ? p[b * 4 + i] : NEG_INF;
+        }
       }
     }
     float mx = p[0];
@@ -1109,6 +1123,7 @@ __global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(Args a) {
   constexpr int THREADS = 64 * tile_waves<D>();
   constexpr int BM = THREADS / 2 / CW, BN = tile_positions<D>();
   constexpr int NB = BN / 32 / CW;
+  constexpr bool TWICE = WIN && D < 256;  // see below
   constexpr int ES = KV8 ? 1 : 2;
   constexpr int CPR = D * ES / 16;       // 16-byte chunks of a cache row
   constexpr int NI = BN * CPR / THREADS; // chunks per thread, tile and operand
@@ -1161,10 +1176,6 @@ __global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(Args a) {
       for (int ks = 0; ks < D / 16; ++ks)
         w.q[ks] = scaled_q(*(const i32x4*)(qp + ks * 16), j.flip, j.none || !r.live);
     }
-    w.m = NEG_INF;
-    w.l = 0.f;
-#pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt) clear(w.o[dt]);
 
     // The cache rows that this thread loads of a tile: chunk idx of the tile
     // in LDS order is row idx / CPR (and, loaded directly, holds the chunk
@@ -1238,6 +1249,17 @@ __global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(Args a) {
       }
     };
 
+    // With a window, the first pass takes values as they are: an infinity or NaN that
+    // some row does not see then shows in its sum (as one that it sees does), and a
+    // second pass tells them apart.  (Looking at all values of every masked tile
+    // cost 161 us instead of 143 for 1500 nodes in two splits, window 1024; at dim
+    // 256 the second pass cost registers instead.)
+    bool careful = false;
+  again_with_care:
+    w.m = NEG_INF;
+    w.l = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < D / 32; ++dt) clear(w.o[dt]);
     if constexpr (KV8) {
       pg = load_pages(0);
       issue(0, pg);
@@ -1278,7 +1300,8 @@ __global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(Args a) {
           const int shift = span.shift(lo + it * BN);
           w.template softmax<TAIL>(p, pf, a, j, node, mrow, lo + it * BN + (b0 + k) * 32 + shift, hi + shift, low,
                                    lane);
-          w.template values<TAIL>(pf, sk + TILE, (b0 + k) * 32, lane);
+          if (TAIL && TWICE && !careful) w.template values<false>(pf, sk + TILE, (b0 + k) * 32, lane);
+          else w.template values<TAIL>(pf, sk + TILE, (b0 + k) * 32, lane);
           if (k + 1 < NB) w.scores(p, sk, (b0 + k + 1) * 32, lane);
         }
       }
@@ -1299,6 +1322,17 @@ __global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(Args a) {
       for (; it < ntl; ++it) step(it, std::true_type{});
     }
     __syncthreads();
+    if constexpr (TWICE) {
+      bool odd = false;
+#pragma unroll
+      for (int dt = 0; dt < D / 32; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) odd |= !(fabsf(w.o[dt][i]) < -NEG_INF);
+      if (!careful && __syncthreads_or(odd && my_row().live)) {
+        careful = true;
+        goto again_with_care;
+      }
+    }
 
     w.l = half_sum(w.l);
     w.m *= j.sc;

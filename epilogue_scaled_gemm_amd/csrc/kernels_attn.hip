@@ -4,10 +4,60 @@
 
 namespace lg {
 
+namespace {
+
+// What the rows of a tile of so many nodes count over with a window at most: sinks
+// and window end in blocks of up to 128.
+int64_t window_reach(int64_t window, int64_t sinks, int64_t nodes) { return sinks + window + nodes + 256; }
+
+// The tile kernel with a window: how many positions a row tile goes over hardly
+// depends on the context, so whole rounds of 256 workgroups count, and parts of
+// splits, which go through memory, cost more than they do over long contexts.
+// The form with the least of
+//   rounds (start + per 128 positions) + (splits > 1: 4 + parts written and read)
+// in us.  Measured with 32 query and 8 key heads of 128: 2 x 1500 nodes over 5001
+// positions, window 1024: 256 rows whole 119 us, in two splits 167, 128 rows 135;
+// 8 trees of 64 nodes: 69, 55, 48 and (128 rows in two splits) 46; 200 nodes: 55,
+// 40, 41 and (128 rows in four splits) 30.
+AttnPlan window_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len, int64_t all_rows,
+                     int64_t window, int64_t sinks, bool masked) {
+  AttnPlan best;
+  double least = 0;
+  const int64_t rows = max_nodes * G;
+  const int64_t most = std::max<int64_t>(1, ((int64_t)1 << 27) / (all_rows * (D + 2) * (int64_t)sizeof(float)));
+  for (int shape : {AT_TILE128, AT_TILE256}) {
+    if (shape == AT_TILE256 && (D == 256 || rows <= 32)) continue;
+    const int bm = attn_rows(shape);
+    // a tile holds bm / G nodes and parts of two more, or a whole tree
+    const int64_t nodes = masked ? max_nodes : std::min<int64_t>(max_nodes, bm / G + 2);
+    const int64_t len = std::min(max_len, window_reach(window, sinks, nodes));
+    const int64_t tiles = (rows + bm - 1) / bm, units = B * Hk * tiles;
+    const int64_t steps = (len + 127) / 128;  // whole blocks of any kernel
+    const double start = shape == AT_TILE128 && D < 256 ? 9 : 15;
+    const double per = D == 256 ? 17.7 : shape == AT_TILE256 ? (D == 64 ? 3.8 : 4.9) : (D == 64 ? 2.5 : 3.7);
+    for (int64_t n = 1; n <= std::min({(int64_t)16, steps, most}); ++n) {
+      const int64_t each = (steps + n - 1) / n;
+      if ((steps + each - 1) / each != n) continue;  // the same cut as with fewer
+      double t = (double)((units * n + 255) / 256) * (start + per * (double)each);
+      if (n > 1) t += 4 + (double)(n * all_rows * D) * 8 / 4.5e6;
+      if (least > 0 && t >= least) continue;
+      least = t;
+      best = {shape, false, tiles, n, each * 128};
+    }
+  }
+  return best;
+}
+
+}  // namespace
+
 AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len,
                    int64_t all_rows, int64_t window, int64_t sinks, bool masked) {
   AttnPlan p;
   const int64_t rows = max_nodes * G;
+  if (window > 0) {
+    if (rows > 16) return window_plan(B, Hk, G, D, max_nodes, max_len, all_rows, window, sinks, masked);
+    max_len = std::min(max_len, window_reach(window, sinks, max_nodes));
+  }
   // (Measured at dim 128 over 16-bit caches of thousands of positions; the other
   // dims, codes and short contexts follow the same borders unmeasured.)
   // 8 trees over 8000 positions (dim 128, bf16), rows of a key head: 32 rows
@@ -18,13 +68,8 @@ AttnPlan attn_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t m
   else p.shape = rows <= 16 ? AT_STREAM16 : rows <= 128 ? AT_TILE128 : AT_TILE256;
   const int bm = attn_rows(p.shape);
   p.ntiles = (rows + bm - 1) / bm;
-  // What the rows of a tile count over with a window: a tile holds bm / G nodes and
-  // parts of two more, or a whole tree; sinks and window end in blocks of up to 128.
-  if (window > 0)
-    max_len = std::min(max_len, sinks + window + (masked ? max_nodes : std::min<int64_t>(max_nodes, bm / G + 2)) + 256);
   const int64_t units = B * Hk * p.ntiles;
-  // positions of one round of the waves; with a window, whole blocks of any kernel
-  const int64_t step = p.shape == AT_STREAM16 || window > 0 ? 128 : 64;
+  const int64_t step = p.shape == AT_STREAM16 ? 128 : 64;  // positions of one round of the waves
   const int64_t steps = (max_len + step - 1) / step;
   // Parts of splits take 128 MB at most, so that a call's workspace is bounded.
   // (With 32 heads of 128: 2100 nodes over 5000 positions take 390 us in nine
