@@ -36,6 +36,14 @@ __device__ inline void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// A barrier that waits for the waves' LDS accesses, but for none of their loads.
+__device__ inline void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Calls f(id, mask of its rows) for the adapters of the window, -1 among them, that
 // are a slot's: the i-th in the order of their first rows belongs to slot i % slots.
 // id and mask are scalar.
@@ -457,7 +465,7 @@ __global__ __launch_bounds__(64 * EX_WAVES, 4) void expand_kernel(LoraArgs a) {
       return;
     }
     Adder<F16, KS, VEC, EX_WAVES> adder(a, id, row0, list, count, c.col0, c.width, c.blk0, c.blk1);
-    __syncthreads();  // (the last adapter's parts are not read any more)
+    lds_barrier();  // (the last adapter's parts are not read any more)
     split_rows<F16, KS, 64 * EX_WAVES>(a, a.factors ? a.factors[id] : 1.f, 0, count, parts, factor,
                                        [&](int p, int r, float* h) {
       const float* at = a.h + (row0 + list[p]) * a.SR + c.slice * a.R + r;
@@ -470,7 +478,7 @@ __global__ __launch_bounds__(64 * EX_WAVES, 4) void expand_kernel(LoraArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[e] = e < 4 ? u[e] : v[e - 4];
     });
-    __syncthreads();
+    lds_barrier();
     adder.run(parts, factor, tiles[wave]);
   });
 }
@@ -521,20 +529,20 @@ __global__ __launch_bounds__(64 * ST_WAVES, 1) void step_kernel(LoraArgs a) {
 #pragma unroll 1
     for (int g = 0; g * 16 < count; ++g) {
       f32x4 acc[L::JT][1];
-      __syncthreads();  // (tiles and sums of before are not read any more)
+      lds_barrier();  // (tiles and sums of before are not read any more)
       shrink_products<F16, L::JT, 1, ST_WAVES>(a, A, c.slice * a.R, row0, list, count, g, 0, (a.K + 63) >> 6,
                                                shared + wave * L::STAGE, acc);
-      __syncthreads();
+      lds_barrier();
 #pragma unroll
       for (int j = 0; j < L::JT; ++j) sums[(wave * L::JT + j) * 64 + lane] = acc[j][0];
-      __syncthreads();
+      lds_barrier();
       for (int j = wave; j < L::JT; j += ST_WAVES) {
         f32x4 v = sums[j * 64 + lane];
 #pragma unroll
         for (int w = 1; w < ST_WAVES; ++w) v += sums[(w * L::JT + j) * 64 + lane];
         *(f32x4*)(hs + (lane & 15) * L::H_ROW + j * 16 + (lane >> 4) * 4) = v;
       }
-      __syncthreads();
+      lds_barrier();
       split_rows<F16, KS, 64 * ST_WAVES>(a, f, g * 16, min(g * 16 + 16, count), parts, factor,
                                          [&](int p, int r, float* h) {
         const float* const at = hs + (p & 15) * L::H_ROW + r;
@@ -542,7 +550,7 @@ __global__ __launch_bounds__(64 * ST_WAVES, 1) void step_kernel(LoraArgs a) {
         for (int e = 0; e < 8; ++e) h[e] = at[e];
       });
     }
-    __syncthreads();
+    lds_barrier();
     adder.run(parts, factor, (float*)shared + wave * TILE_VALUES);
   });
 }
