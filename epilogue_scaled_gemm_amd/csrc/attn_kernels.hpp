@@ -177,8 +177,8 @@ struct Job {
 // What lies beyond the page table (at most 2^30 positions) is cut off.
 __device__ inline void set_lengths(const AttnArgs& a, Job& j) {
   const int most = a.max_pages << a.page_log;
+  j.ctx = min(max(a.context[j.b], 0), most);
   j.pos0 = min(max(a.context[j.b], 0), 1 << 30);
-  j.ctx = min(j.pos0, most);
   j.len = min(j.ctx + j.n, most);
 }
 
@@ -902,12 +902,41 @@ template <int D> __device__ inline int v_off(int row, int chunk) {
 typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(1))) const void global_void;
 
+// Where the chunk that a fragment needs is XOR-ed with the lane's row, the XOR of a
+// lane's own part and the fragment's is one instruction with the sum of the
+// tile's place (XOR = true: nothing else is computed for a read; written as an
+// offset, rows and chunks were computed again for most of them).
+__device__ inline uint32_t lds_address(const char* p) { return (uint32_t)(uintptr_t)(lds_char*)p; }
+typedef __attribute__((address_space(3))) const i32x4 lds_i32x4;
+
+// The key fragment f of a block of 32 positions that starts at row r0.
+template <int D, bool XOR>
+__device__ inline i32x4 key_frag(const char* sk, int r0, int f, int col, int half) {
+  if constexpr (XOR) {
+    const uint32_t own = col * (D * 2) + ((half ^ (col & (D / 8 - 1))) << 4);
+    return *(lds_i32x4*)((own ^ (uint32_t)(f << 5)) + lds_address(sk) + r0 * (D * 2));
+  } else {
+    return *(const i32x4*)(sk + k_off<D>(r0 + col, 2 * f + half));
+  }
+}
+
 // The value fragment f of a block of 32 positions that starts at row `r0` of
 // a tile: sixteen positions (f / DT) by 32 values (f % DT), by two transposing
 // reads per lane.
-template <int D> __device__ inline i32x4 value_frag(const char* sv, int r0, int f, int lane) {
+template <int D, bool XOR = false>
+__device__ inline i32x4 value_frag(const char* sv, int r0, int f, int lane) {
   constexpr int DT = D / 32;
   const int i16 = lane & 15;
+  if constexpr (XOR) {
+    // rows 8 and more apart have the same XOR
+    const int rr = 4 * (lane >> 5) + (i16 >> 2), c0 = 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
+    const uint32_t own = rr * (D * 2) + ((c0 ^ v_xor<D>(rr)) << 4) + (i16 & 1) * 8;
+    const uint32_t at = (own ^ (uint32_t)(f % DT << 6)) + lds_address(sv) + (r0 + 16 * (f / DT)) * (D * 2);
+    const i32x2 w0 = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at));
+    const i32x2 w1 =
+        __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 8 * (D * 2))));
+    return i32x4{w0[0], w0[1], w1[0], w1[1]};
+  }
   const int r = r0 + 16 * (f / DT) + 4 * (lane >> 5) + (i16 >> 2);
   const int c = 4 * (f % DT) + 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
   const int b8 = (i16 & 1) * 8;
@@ -933,6 +962,7 @@ template <int D, bool F16> struct Rows {
 
   // Scores of a block of 32 positions.  Key fragments are read a few ahead of
   // the products that use them.
+  template <bool XOR>
   __device__ inline ALWAYS_INLINE void scores(f32x16& p, const char* sk, int r0, int lane) {
     constexpr int KA = 4;
     if constexpr (D == 256) lane = again(lane);
@@ -940,11 +970,11 @@ template <int D, bool F16> struct Rows {
     i32x4 kf[KS];
     clear(p);
 #pragma unroll
-    for (int f = 0; f < KA; ++f) kf[f] = *(const i32x4*)(sk + k_off<D>(r0 + col, 2 * f + half));
+    for (int f = 0; f < KA; ++f) kf[f] = key_frag<D, XOR>(sk, r0, f, col, half);
 #pragma unroll
     for (int f = 0; f < KS; ++f) {
       p = mfma32<F16>(kf[f], q[f], p);
-      if (f + KA < KS) kf[f + KA] = *(const i32x4*)(sk + k_off<D>(r0 + col, 2 * (f + KA) + half));
+      if (f + KA < KS) kf[f + KA] = key_frag<D, XOR>(sk, r0, f + KA, col, half);
     }
   }
   // Masks (for the positions pos + ... of the block), running maximum and sum;
@@ -998,14 +1028,14 @@ template <int D, bool F16> struct Rows {
   }
   // O^T += V^T P^T for the block.  TAIL: values that some rows do not see, or
   // that lie past the end, may be infinite or NaN.
-  template <bool TAIL>
+  template <bool TAIL, bool XOR>
   __device__ inline ALWAYS_INLINE void values(const i32x4 (&pf)[2], const char* sv, int r0, int lane) {
     constexpr int NF = 2 * DT, VA = 4 < NF ? 4 : NF;
     if constexpr (D == 256) lane = again(lane);
     if constexpr (TAIL) {
       bool odd = false;
 #pragma unroll
-      for (int f = 0; f < NF; ++f) odd |= not_finite8<F16>(value_frag<D>(sv, r0, f, lane));
+      for (int f = 0; f < NF; ++f) odd |= not_finite8<F16>(value_frag<D, XOR>(sv, r0, f, lane));
       if (__any(odd)) {
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) {
@@ -1015,14 +1045,14 @@ template <int D, bool F16> struct Rows {
             clear(t);
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt)
-              t = mfma32<F16>(where_kind<F16>(value_frag<D>(sv, r0, tt * DT + dt, lane), kind),
+              t = mfma32<F16>(where_kind<F16>(value_frag<D, XOR>(sv, r0, tt * DT + dt, lane), kind),
                               pf[tt], t);
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[dt][i] += t[i] > 0.f ? kind_value(kind) : 0.f;
           }
 #pragma unroll
           for (int tt = 0; tt < 2; ++tt)
-            o[dt] = mfma32<F16>(finite_part<F16>(value_frag<D>(sv, r0, tt * DT + dt, lane)), pf[tt],
+            o[dt] = mfma32<F16>(finite_part<F16>(value_frag<D, XOR>(sv, r0, tt * DT + dt, lane)), pf[tt],
                                 o[dt]);
         }
         return;
@@ -1030,11 +1060,11 @@ template <int D, bool F16> struct Rows {
     }
     i32x4 vf[NF];
 #pragma unroll
-    for (int f = 0; f < VA; ++f) vf[f] = value_frag<D>(sv, r0, f, lane);
+    for (int f = 0; f < VA; ++f) vf[f] = value_frag<D, XOR>(sv, r0, f, lane);
 #pragma unroll
     for (int f = 0; f < NF; ++f) {
       o[f % DT] = mfma32<F16>(vf[f], pf[f / DT], o[f % DT]);
-      if (f + VA < NF) vf[f + VA] = value_frag<D>(sv, r0, f + VA, lane);
+      if (f + VA < NF) vf[f + VA] = value_frag<D, XOR>(sv, r0, f + VA, lane);
     }
   }
   // Writes a finished row, or its part of a split one.
@@ -1123,7 +1153,7 @@ __global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(Args a) {
   constexpr int THREADS = 64 * tile_waves<D>();
   constexpr int BM = THREADS / 2 / CW, BN = tile_positions<D>();
   constexpr int NB = BN / 32 / CW;
-  constexpr bool TWICE = WIN && D < 256;  // see below
+  constexpr bool TWICE = WIN && D < 256, XOR = WIN;  // see below
   constexpr int ES = KV8 ? 1 : 2;
   constexpr int CPR = D * ES / 16;       // 16-byte chunks of a cache row
   constexpr int NI = BN * CPR / THREADS; // chunks per thread, tile and operand
@@ -1155,11 +1185,14 @@ __global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(Args a) {
     const int nsp = split_range(a, j, count_positions<BN>(a, j, row0 / a.G, last, span), lo, hi);
     if (j.split >= nsp) continue;
     const int ntl = (hi - lo + BN - 1) / BN;
-    // tiles that every row sees whole: the first ones, or, with a window, some in
-    // the middle
-    const int all = min(a.mask ? j.ctx : j.ctx + row0 / a.G + 1, hi + (WIN ? span.shift(hi) : 0));
+    // tiles [first, full) that every row sees whole
+    int first = 0;
+    int all = min(a.mask ? j.ctx : j.ctx + row0 / a.G + 1, hi);
+    if constexpr (WIN) {  // (all tiles before the gap end before span.whole)
+      all = min((a.mask ? j.ctx : j.ctx + row0 / a.G + 1) - span.gap, hi);
+      first = max(0, (span.whole - span.gap - lo + BN - 1) / BN);
+    }
     const int full = max(0, (all - lo) / BN);
-
     // this lane's row (rows past the end stand for the first and are not stored)
     struct Row { bool live; int node, head; };
     auto my_row = [&]() ALWAYS_INLINE {
@@ -1279,9 +1312,9 @@ __global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(Args a) {
     f32x16 p;
     i32x4 pf[2];
     const bool busy = row0 + rw * 32 < nrows;  // any live row in this wave
-    w.scores(p, buffer(0), b0 * 32, lane);
-    auto step = [&](int it, auto tail_tag) ALWAYS_INLINE {
-      constexpr bool TAIL = decltype(tail_tag)::value;
+    w.template scores<XOR>(p, buffer(0), b0 * 32, lane);
+    auto step = [&](int it, auto tail_tag, auto look_tag) ALWAYS_INLINE {
+      constexpr bool TAIL = decltype(tail_tag)::value, LOOK = decltype(look_tag)::value;
       const char* const sk = buffer(it);
       if (!KV8 && it + 3 < ntl) {
         issue(it + 3, pg);
@@ -1300,26 +1333,37 @@ __global__ __launch_bounds__(64 * tile_waves<D>()) void tile_kernel(Args a) {
           const int shift = span.shift(lo + it * BN);
           w.template softmax<TAIL>(p, pf, a, j, node, mrow, lo + it * BN + (b0 + k) * 32 + shift, hi + shift, low,
                                    lane);
-          if (TAIL && TWICE && !careful) w.template values<false>(pf, sk + TILE, (b0 + k) * 32, lane);
-          else w.template values<TAIL>(pf, sk + TILE, (b0 + k) * 32, lane);
-          if (k + 1 < NB) w.scores(p, sk, (b0 + k + 1) * 32, lane);
+          w.template values<TAIL && LOOK, XOR>(pf, sk + TILE, (b0 + k) * 32, lane);
+          if (k + 1 < NB) w.template scores<XOR>(p, sk, (b0 + k + 1) * 32, lane);
         }
       }
       finish(it + 1, 2);
       tile_barrier();
       // (past the last block: of whatever the next buffer holds, not used)
-      if (busy) w.scores(p, buffer(it + 1), b0 * 32, lane);
+      if (busy) w.template scores<XOR>(p, buffer(it + 1), b0 * 32, lane);
     };
     if constexpr (WIN) {
-      for (int it = 0; it < ntl; ++it) {
-        const int at = lo + it * BN, base = at + span.shift(at);
-        if (base >= span.whole && base + BN <= all && at + BN <= hi) step(it, std::false_type{});
-        else step(it, std::true_type{});
+      if (TWICE && careful) {
+#pragma unroll 1
+        for (int it = 0; it < ntl; ++it) step(it, std::true_type{}, std::true_type{});
+      } else {
+        // masked tiles, whole ones, masked ones.  (Chosen tile by tile, the two kinds of
+        // a step keep their sums in registers of their own and copy them: 1500 nodes
+        // over 5001 positions 125 us instead of 112.)
+        int it = 0, stop = min(first, ntl);
+#pragma unroll 1
+        for (;; stop = ntl) {
+#pragma unroll 1
+          for (; it < stop; ++it) step(it, std::true_type{}, std::bool_constant<!TWICE>{});
+#pragma unroll 1
+          for (; it < full; ++it) step(it, std::false_type{}, std::false_type{});
+          if (stop == ntl) break;
+        }
       }
     } else {
       int it = 0;
-      for (; it < full; ++it) step(it, std::false_type{});
-      for (; it < ntl; ++it) step(it, std::true_type{});
+      for (; it < full; ++it) step(it, std::false_type{}, std::false_type{});
+      for (; it < ntl; ++it) step(it, std::true_type{}, std::true_type{});
     }
     __syncthreads();
     if constexpr (TWICE) {
