@@ -16,12 +16,13 @@ int64_t window_reach(int64_t window, int64_t sinks, int64_t nodes) { return sink
 // The form with the least of
 //   rounds (start + per 128 positions) + (splits > 1: 4 + parts written and read)
 // in us.  Measured with 32 query and 8 key heads of 128: 2 x 1500 nodes over 5001
-// positions, window 1024: 256 rows whole 119 us, in two splits 167, 128 rows 135;
-// 8 trees of 64 nodes: 69, 55, 48 and (128 rows in two splits) 46; 200 nodes: 55,
-// 40, 41 and (128 rows in four splits) 30.
+// positions, window 1024: 256 rows whole 106 us, 128 rows 109 and in two splits 175;
+// window 4096: 288 and 285; 8 trees of 64 nodes: 61, 42 and 43; 200 nodes: 49, 34
+// and (128 rows in four splits) 28.  Dim 64, 2 x 1500 nodes: 85 and 82; dim 256,
+// 2 x 700: 94 whole, 77 in two splits.
 AttnPlan window_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len, int64_t all_rows,
                      int64_t window, int64_t sinks, bool masked) {
-  AttnPlan best;
+  AttnPlan best = {AT_TILE128, false, 1, 1, 128};
   double least = 0;
   const int64_t rows = max_nodes * G;
   const int64_t most = std::max<int64_t>(1, ((int64_t)1 << 27) / (all_rows * (D + 2) * (int64_t)sizeof(float)));
@@ -33,8 +34,8 @@ AttnPlan window_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t
     const int64_t len = std::min(max_len, window_reach(window, sinks, nodes));
     const int64_t tiles = (rows + bm - 1) / bm, units = B * Hk * tiles;
     const int64_t steps = (len + 127) / 128;  // whole blocks of any kernel
-    const double start = shape == AT_TILE128 && D < 256 ? 9 : 15;
-    const double per = D == 256 ? 17.7 : shape == AT_TILE256 ? (D == 64 ? 3.8 : 4.9) : (D == 64 ? 2.5 : 3.7);
+    const double start = D == 256 ? 23 : shape == AT_TILE256 ? 11 : 8;
+    const double per = D == 256 ? 6.7 : shape == AT_TILE256 ? (D == 64 ? 2.7 : 3.75) : (D == 64 ? 1.85 : 2.5);
     for (int64_t n = 1; n <= std::min({(int64_t)16, steps, most}); ++n) {
       const int64_t each = (steps + n - 1) / n;
       if ((steps + each - 1) / each != n) continue;  // the same cut as with fewer
