@@ -5,19 +5,22 @@
 //   h[t, r] = sum_k x[t, k] A[id, r, k],        id = ids[t]
 //
 // (a QKV product's slices have their own rows of A: h then is [slices][rank]).
-// Two launches: shrink_kernel forms h in 32 bits, expand_kernel adds its
-// product with B to the base and rounds once.
+// Two launches: shrink_kernel forms h in 32 bits, expand_kernel adds its product
+// with B to the base and rounds once; few rows take both steps in one launch
+// (step_kernel).
 //
 // Rows name their adapters in any order.  A window of 64 rows is one id per lane,
-// so that the rows of one adapter are a ballot: a workgroup takes adapters whose
-// first row of the window lies in its slot, gathers their rows as MFMA columns
-// and so reads an adapter's weights once for all its rows of the window.  Rows
-// and weights go from memory straight into MFMA operands (16x16x32: weights are
-// the rows, tokens the columns); every wave has loads of several steps on their
-// way.
+// so that the rows of one adapter are a ballot: a workgroup takes adapters of a
+// window, gathers their rows as MFMA columns (16x16x32: rows of A and B are the
+// rows, tokens the columns) and so reads an adapter's weights once for all its rows
+// of the window.
 //
-// Bound by bytes: of the adapters in use for a decode step, of x, base and out
-// for prompts.
+// Bound by bytes: x once, base and out once, the weights of the adapters in use.
+// 8191 rows of a 6144-wide QKV product (K = 4096, rank 32, bf16) take 21 us for h
+// (3.2 TB/s of x; A comes from the caches for every window) and 46 for the rest (4.4
+// TB/s; a large copy reaches 5.1); 300 rows of N = 4099, whose rows are not aligned,
+// 7 and 13.  A decode step is a chain of latencies: ids, rows of x and A (131 KB
+// for one CU at rank 16), the waves' sums, parts, output: 7 us for one row.
 #include "launch.hpp"
 
 namespace lg {
@@ -570,9 +573,7 @@ template <bool F16, bool VEC> hipError_t launch_type(const LoraArgs& a, const Lo
   const int ks = a.R <= 16 ? 0 : (a.R + 31) / 32;
   const dim3 out_grid(windows, chunks);
   if (p.step) {
-    if (ks == 0) return launch_step<F16, 0, VEC>(a, out_grid, s);
-    if (ks == 1) return launch_step<F16, 1, VEC>(a, out_grid, s);
-    return launch_step<F16, 2, VEC>(a, out_grid, s);
+    return ks ? launch_step<F16, 1, VEC>(a, out_grid, s) : launch_step<F16, 0, VEC>(a, out_grid, s);
   }
   const dim3 grid(windows, (unsigned)((a.SR + 16 * p.tiles - 1) / (16 * p.tiles)), a.ksplit);
   const dim3 in_block(64 * SH_WAVES), block(64 * EX_WAVES);
@@ -607,21 +608,28 @@ LoraPlan lora_plan(int64_t T, int64_t K, const int* width, int S, int R, int64_t
   const int64_t groups = windows * p.slots;
   int64_t blocks = 0;
   for (int i = 0; i < S; ++i) blocks += (width[i] + 63) / 64;
-  // Few rows, and no more reads of A by all chunks than the caches give quickly.
-  p.step = T <= LR_WINDOW && R <= 64 && groups * ((blocks + 7) / 8) * R * K * 2 <= (int64_t)1 << 25;
+  // One launch for few rows.  Each of its workgroups reads its slice of A by itself and
+  // takes 16 rows of an adapter at a time, and a CU holds one: up to two rounds of
+  // them, ranks up to 32, about eight rows to an adapter.  (K = N = 4096, rank 16, us
+  // in one launch and in two: 1 row 10 and 12, 48 rows of 24 adapters 11 and 17, 64 of
+  // 64 20 and 22; 64 rows of two adapters 23 and 12, 32 of 32 with N = 14336 35 and
+  // 18; rank 64: 1 row 12.5 and 12.4, 16 of 16 adapters 14 and 12.)
+  p.step = T <= LR_WINDOW && R <= 32 && (T <= 16 || T <= 8 * n) && groups * ((blocks + 7) / 8) <= 2 * 256 + 16;
   p.tiles = p.ksteps = p.ksplit = 1;
   p.blocks = 8;
   if (p.step) return p;
   const int tiles = (SR + 15) / 16;
   const int64_t parts = (tiles + 3) / 4;
   p.tiles = (tiles + parts - 1) / parts;
-  // k is split until about 512 workgroups have work, but for no less than two steps
-  // of 64 for each wave.
+  // k is split until about 512 workgroups have work (8191 rows of K = 4096, three slices
+  // of rank 32, both launches: 67 us, and 74 with 256, 75 with 1024), but for no less
+  // than two steps of 64 for each wave.
   const int64_t steps = (K + 63) / 64, busy = groups * parts;
   const int64_t want = std::min<int64_t>((512 + busy - 1) / busy, 32);
   p.ksteps = std::max<int64_t>((steps + want - 1) / want, 2 * SH_WAVES);
   p.ksplit = (steps + p.ksteps - 1) / p.ksteps;
-  // blocks of columns per workgroup: about 2048 workgroups
+  // blocks of columns per workgroup: about 2048 workgroups (the same call: 84 us with 512,
+  // 71 with 4096; 2000 rows of rank 64 54, 35 and 33)
   p.blocks = 1;
   while (p.blocks < 64 && groups * (blocks / p.blocks) > 2048) p.blocks *= 2;
   return p;

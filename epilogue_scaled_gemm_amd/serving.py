@@ -103,9 +103,10 @@ def _rows(name, t, shape, dtype):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)} (no broadcasting), got {list(t.shape)}")
-    if shape[1] > 1 and t.stride(1) != 1:
+    rs, vs = t.stride()
+    if vs != 1 and shape[1] > 1:
         raise ValueError(f"{name}: the values of a row must be contiguous")
-    return _at(name, t), t.stride(0) if shape[0] > 1 else 0
+    return _at(name, t), rs if shape[0] > 1 else 0
 
 
 def _cache_type(k_cache, dtype, k_scale, v_scale):

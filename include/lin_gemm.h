@@ -479,8 +479,9 @@ typedef struct {
  * At least one of residual_out, out and codes is asked for.  Addresses and
  * row strides are multiples of 16 bytes; width is a multiple of 16 with codes
  * per token and of 128 with codes per block.  A row with an infinity or NaN
- * gives what the formula gives in out, unspecified codes and scales.  No
- * allocation. */
+ * gives what the formula gives in out, unspecified codes and scales (so does
+ * a row of zeros with an eps of zero).  Outputs overlap inputs only as said,
+ * at the same address and stride.  No allocation. */
 int lin_gemm_add_rms_norm(lin_gemm_t h, const lin_norm_t *args, void *stream);
 
 typedef struct {
@@ -512,7 +513,8 @@ typedef struct {
  * and v of a QKV product).  Rows name adapters in any order; rows of one
  * adapter that lie near each other read its weights once.  Rows without an
  * adapter get the base.  h is binary32 and enters the second product with 16
- * bits or more; sums are binary32, the result is rounded once.  inner is a
+ * bits or more; sums are binary32, the result is rounded once.  out overlaps
+ * no other operand but, at the same address and stride, the base.  inner is a
  * multiple of 8, x and its stride, a and b multiples of 16 bytes; base and
  * out need the alignment of their elements only (16-byte rows and slices
  * are faster).  inner and width up to 2^20.  h goes to the handle's
