@@ -320,18 +320,20 @@ template <bool F16, int KS, bool VEC, int WAVES> struct Adder {
   __device__ inline void load() {
     const int n0 = (blk0 + unit / gs) * 64, g0 = unit % gs * GROUPS, col = lane() & 15, q = lane() >> 4;
     const int n = column();
-    if constexpr (VEC) {
+    if (a.base) {  // (lanes without a value load another instead: see run())
+      if constexpr (VEC) {
 #pragma unroll
-      for (int g = 0; g < GROUPS; ++g)
+        for (int g = 0; g < GROUPS; ++g)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (a.base && inside(n))
-            wide[g][i] =
-                *(const i32x4*)(a.base + row_of((g0 + g) * 16 + i * 8 + (lane() >> 3)) * a.base_s + col0 + n);
-    } else {
+          for (int i = 0; i < 2; ++i) {
+            const uint16_t* const from =
+                a.base + row_of((g0 + g) * 16 + i * 8 + (lane() >> 3)) * a.base_s + col0 + n;
+            wide[g][i] = *(const i32x4*)(inside(n) ? from : B);
+          }
+      } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (a.base && inside(n)) single[i] = a.base[row_of(g0 * 16 + i) * a.base_s + col0 + n];
+        for (int i = 0; i < 16; ++i) single[i] = a.base[row_of(g0 * 16 + i) * a.base_s + col0 + min(n, width - 1)];
+      }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -402,10 +404,17 @@ template <bool F16, int KS, bool VEC, int WAVES> struct Adder {
     }
   }
   __device__ inline void run(const char* parts, const float* factor, float* tile) {
+    // Matrix instructions write all lanes, whether or not they are switched off, so a
+    // wave stays together here.  A condition of a lane's own between one turn and the
+    // next (as "this lane's column is inside" at load()'s loads was) let the compiler
+    // make a loop of its own for the lanes outside, whose products overwrote registers
+    // of the waiting ones, addresses among them.
     while (unit < units) {
       finish(parts, factor, tile);
+      __builtin_amdgcn_wave_barrier();
       unit += WAVES;
       if (unit < units) load();
+      __builtin_amdgcn_wave_barrier();
     }
   }
 };

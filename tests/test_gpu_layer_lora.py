@@ -87,6 +87,14 @@ def test_many_rows_of_one_adapter_among_many_adapters(handle, R, N):
         c.check(c.run(handle))
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("R,N", [(16, 2112), (24, 2101), (32, 2101), (32, 2104), (64, 2101)])
+def test_waves_that_take_several_blocks_of_many_rows(handle, dtype, R, N):
+    # the last block of columns is partial: some lanes of a wave have none, and go on with the others
+    c = Case(4100, 72, N, R, 2, dtype, ids=[1] * 4000 + [0] * 99 + [-1])
+    c.check(c.run(handle))
+
+
 @pytest.mark.parametrize("widths", [(512, 128, 128), (64, 64), (1, 1, 1, 1), (100, 28, 3), (40, 200, 8, 16)])
 @pytest.mark.parametrize("R", [8, 16, 64])
 def test_slices_have_their_own_adapters(handle, widths, R):
