@@ -258,11 +258,14 @@ __device__ inline int count_positions(const Args& a, const Job& j, int first, in
 }
 
 // Positions [lo, hi) of a split, counted, and how many splits the rows have.
+// Windows that begin past the page table leave no position; the first split is
+// there all the same and writes the rows (zeros).
 template <typename Args>
 __device__ inline int split_range(const Args& a, const Job& j, int all, int& lo, int& hi) {
   lo = j.split * a.chunk;
   // the last split takes what the bound did not foresee
   hi = j.split == a.nsplit - 1 ? all : min(all, lo + a.chunk);
+  if constexpr (WINDOWED<Args>) all = max(all, 1);
   return a.nsplit == 1 ? 1 : min(a.nsplit, (all + a.chunk - 1) / a.chunk);
 }
 
