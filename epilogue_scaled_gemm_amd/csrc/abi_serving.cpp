@@ -269,8 +269,8 @@ int run_attention(lin_gemm_t h, const lin_attention_t* p, const lin_window_t* wi
   const int64_t len = std::min(std::min(p->max_context, room) + nodes, room);
   if (win) {
     w.positions = win->positions;
-    w.window = (int)std::min<int64_t>(win->window, (int64_t)1 << 30);  // (of at most 2^30 positions)
-    w.sinks = (int)std::min<int64_t>(win->sinks, (int64_t)1 << 30);
+    w.window = (int)std::min<int64_t>(win->window, 0x7FFFFFFF);     // (beyond every node's position)
+    w.sinks = (int)std::min<int64_t>(win->sinks, (int64_t)1 << 30);  // (of at most 2^30 cached ones)
   }
   const lg::AttnPlan plan =
       lg::attn_plan(p->sequences, a.Hk, a.G, (int)p->dim, nodes, len, a.rows, w.window, w.sinks, a.mask != nullptr);

@@ -178,11 +178,12 @@ struct Job {
   bool flip, none;  // the sign of the scale goes to q; a zero scale: q is 0
 };
 
-// What lies beyond the page table (at most 2^30 positions) is cut off.
+// What lies beyond the page table (at most 2^30 positions) is cut off.  Positions of
+// nodes (at most 2^23) fit 32 bits.
 __device__ inline void set_lengths(const AttnArgs& a, Job& j) {
   const int most = a.max_pages << a.page_log;
   j.ctx = min(max(a.context[j.b], 0), most);
-  j.pos0 = min(max(a.context[j.b], 0), 1 << 30);
+  j.pos0 = min(max(a.context[j.b], 0), 0x7FFFFFFF - (1 << 23));
   j.len = min(j.ctx + j.n, most);
 }
 
@@ -228,13 +229,13 @@ template <typename Args> __device__ inline int in_sinks(const Args& a) {
   else return 0;
 }
 
-// Where the window of a node begins.  The positions of a tree's nodes are
-// clamped to those that its nodes can have.
+// Where the window of a node begins: 0, or further on.  The positions of a tree's
+// nodes are clamped to those that its nodes can have.
 template <typename Args> __device__ inline int window_low(const Args& a, const Job& j, int node) {
   if constexpr (WINDOWED<Args>) {
     int p = j.pos0 + node;
     if (a.mask && a.positions) p = min(max(a.positions[j.t0 + node], j.pos0), j.pos0 + j.n - 1);
-    return p - a.window + 1;
+    return max(p - a.window, -1) + 1;
   } else {
     return 0;
   }
@@ -249,7 +250,7 @@ __device__ inline int count_positions(const Args& a, const Job& j, int first, in
   if constexpr (WINDOWED<Args>) {
     const int low = j.pos0 - a.window + 1;  // of node 0
     const int from = min(max(a.mask ? low : low + first, 0), all);
-    span.whole = a.mask ? low + j.n - 1 : low + last;
+    span.whole = max(a.mask ? low + j.n - 1 : low + last, 0);
     span.seam = (min(a.sinks, all) + BLOCK - 1) / BLOCK * BLOCK;
     span.gap = max(from / BLOCK * BLOCK - span.seam, 0);
     all -= span.gap;

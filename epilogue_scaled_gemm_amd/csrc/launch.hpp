@@ -208,7 +208,7 @@ hipError_t launch_attention(const AttnArgs& a, int D, int shape, bool f16, bool 
 // positions c < sinks and c > p - window.
 struct WindowArgs : AttnArgs {
   const int* positions;    // [T] of the nodes of trees, or null: context + node
-  int window, sinks;       // 1 .. 2^30, 0 .. 2^30
+  int window, sinks;       // 1 .. 2^31 - 1, 0 .. 2^30
 };
 hipError_t launch_window(const WindowArgs& a, int D, int shape, bool f16, bool kv8, hipStream_t s);
 

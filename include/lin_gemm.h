@@ -421,7 +421,8 @@ typedef struct {
  * row sees, they are seen whatever the window; it applies to the context.
  * Positions that no row sees are not read, but for those that share a block
  * of 128 with a visible one, whose values do not reach the result: page table
- * entries of dropped pages may hold anything. */
+ * entries of dropped pages may hold anything.  Contexts may lie beyond the page
+ * table, up to 2^31 - 2^23 positions. */
 int lin_gemm_window_attention(lin_gemm_t h, const lin_window_t *args, void *stream);
 
 typedef struct {
