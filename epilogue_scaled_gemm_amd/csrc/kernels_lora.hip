@@ -20,7 +20,8 @@
 // (3.2 TB/s of x; A comes from the caches for every window) and 46 for the rest (4.4
 // TB/s; a large copy reaches 5.1); 300 rows of N = 4099, whose rows are not aligned,
 // 7 and 13.  A decode step is a chain of latencies: ids, rows of x and A (131 KB
-// for one CU at rank 16), the waves' sums, parts, output: 7 us for one row.
+// for one CU at rank 16), the waves' sums, parts, output: 8.7 us in the kernel for one
+// row, of which a workgroup's first to last instruction take 6.8.
 #include "launch.hpp"
 
 namespace lg {
@@ -611,7 +612,9 @@ LoraPlan lora_plan(int64_t T, int64_t K, const int* width, int S, int R, int64_t
   const int SR = S * R;
   const int64_t windows = (T + LR_WINDOW - 1) / LR_WINDOW;
   // A workgroup for each adapter that a window can have, up to about 256 of them; one
-  // for all where there are windows enough (most of the others would find none).
+  // for all from 64 windows on.  That is for runs of rows, where most of the others
+  // would find none (4096 rows, three slices of 6144 columns, rank 16, 16 adapters: 46 us
+  // and 62 with four slots a window); for rows in any order it costs (198 us and 112).
   const int64_t distinct = std::min({T, n + 1, (int64_t)LR_WINDOW});
   p.slots = windows >= 64 ? 1 : std::max<int64_t>(1, std::min(distinct, 256 / windows));
   const int64_t groups = windows * p.slots;
@@ -619,20 +622,28 @@ LoraPlan lora_plan(int64_t T, int64_t K, const int* width, int S, int R, int64_t
   for (int i = 0; i < S; ++i) blocks += (width[i] + 63) / 64;
   // One launch for few rows.  Each of its workgroups reads its slice of A by itself and
   // takes 16 rows of an adapter at a time, and a CU holds one: up to two rounds of
-  // them, ranks up to 32, about eight rows to an adapter.  (K = N = 4096, rank 16, us
-  // in one launch and in two: 1 row 10 and 12, 48 rows of 24 adapters 11 and 17, 64 of
-  // 64 20 and 22; 64 rows of two adapters 23 and 12, 32 of 32 with N = 14336 35 and
-  // 18; rank 64: 1 row 12.5 and 12.4, 16 of 16 adapters 14 and 12.)
-  p.step = T <= LR_WINDOW && R <= 32 && (T <= 16 || T <= 8 * n) && groups * ((blocks + 7) / 8) <= 2 * 256 + 16;
+  // them, ranks up to 32.  (K = N = 4096, rank 16, us a call in one launch and in two: 1
+  // row 8 and 10, 16 rows of 16 adapters 9 and 11, 48 of 24 10 and 17, 64 of 64 22 and
+  // 27.  N = 6144: 504 workgroups for 42 rows 20 and 23, 528 for 44 28 and 20; 32 rows of
+  // 32 with N = 14336 35 and 19.  Rank 64: 1 row 12.5 and 12.4, 16 of 16 14 and 12.)
+  // Beyond 16 rows, up to eight rows for each adapter that there is: how many of
+  // them the rows name is on the device.  Rows that name them all or any at random fit
+  // that (64 rows of 64 adapters, of which 40 are named: 20 and 22 us, 16 16 and 16, 8
+  // 15 and 14; two adapters 23 and 11: two launches by the rule).  One that many rows
+  // share does not: 64 rows of 4 of the 64 take 19 and 14 us, of one 34 and 15, 16 rows
+  // at a time in one workgroup for each 512 columns.
+  p.step = T <= LR_WINDOW && R <= 32 && (T <= 16 || T <= 8 * n) && groups * ((blocks + 7) / 8) <= 2 * 256;
   p.tiles = p.ksteps = p.ksplit = 1;
   p.blocks = 8;
   if (p.step) return p;
   const int tiles = (SR + 15) / 16;
   const int64_t parts = (tiles + 3) / 4;
   p.tiles = (tiles + parts - 1) / parts;
-  // k is split until about 512 workgroups have work (8191 rows of K = 4096, three slices
+  // k is split until there are about 512 workgroups (8191 rows of K = 4096, three slices
   // of rank 32, both launches: 67 us, and 74 with 256, 75 with 1024), but for no less
-  // than two steps of 64 for each wave.
+  // than two steps of 64 for each wave.  Slots that find no adapter count too (300 rows
+  // of 5 of 64 adapters, rank 16: 21 us, and 23 if only windows count; 1000 rows of 10, rank
+  // 32: 27 and 26).
   const int64_t steps = (K + 63) / 64, busy = groups * parts;
   const int64_t want = std::min<int64_t>((512 + busy - 1) / busy, 32);
   p.ksteps = std::max<int64_t>((steps + want - 1) / want, 2 * SH_WAVES);
