@@ -418,38 +418,42 @@ _KINDS = {"fp8_token": torch.float8_e4m3fn, "int8_token": torch.int8,
           "fp8_block": torch.float8_e4m3fn}
 
 
-def _norm_shapes(x, kind):
+def _norm_shapes(x, residual, kind, normed):
     if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError("x must be [rows, width] in bfloat16 or float16")
     if kind and kind not in _KINDS:
         raise ValueError(f"kind must be one of {sorted(_KINDS)} or empty, got {kind!r}")
+    if residual is None and not kind and not normed:
+        raise ValueError("no output is asked for")
     T, N = x.shape
-    return ((T, N), (T, N // 128) if kind == "fp8_block" else (T,)) if kind else ((0,), (0,))
+    return ((T, N) if residual is not None else (0,), (T, N) if normed else (0,),
+            *(((T, N), (T, N // 128) if kind == "fp8_block" else (T,)) if kind else ((0,), (0,))))
 
 
 @torch.library.custom_op("lingemm::add_rms_norm", mutates_args=())
 def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tensor] = None,
-                 kind: str = "", eps: float = 1e-6) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor,
-                                                             torch.Tensor]:
+                 kind: str = "", eps: float = 1e-6,
+                 normed: bool = True) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
     """(x + residual, its norm times weight, the norm's codes, their scales)
-    over rows [T, N]; without a residual the first, without a kind
-    ("fp8_token", "int8_token" or "fp8_block") the last two are empty."""
-    coded, scaled = _norm_shapes(x, kind)
-    out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    total = torch.empty(x.shape if residual is not None else (0,), dtype=x.dtype, device=x.device)
+    over rows [T, N]; without a residual the first, with normed false the
+    second, without a kind ("fp8_token", "int8_token" or "fp8_block") the last
+    two are empty and not computed."""
+    summed, rows, coded, scaled = _norm_shapes(x, residual, kind, normed)
+    total = torch.empty(summed, dtype=x.dtype, device=x.device)
+    out = torch.empty(rows, dtype=x.dtype, device=x.device)
     codes = torch.empty(coded, dtype=_KINDS.get(kind, torch.int8), device=x.device)
     scales = torch.empty(scaled, dtype=torch.float32, device=x.device)
     handle_for(x.device).add_rms_norm(
-        x, weight, residual=residual, residual_out=total if residual is not None else None, out=out,
-        codes=codes if kind else None, scales=scales if kind else None, kind=kind or "fp8_token", eps=eps)
+        x, weight, residual=residual, residual_out=total if residual is not None else None,
+        out=out if normed else None, codes=codes if kind else None, scales=scales if kind else None,
+        kind=kind or "fp8_token", eps=eps)
     return total, out, codes, scales
 
 
 @add_rms_norm.register_fake
-def _add_rms_norm_fake(x, weight, residual=None, kind="", eps=1e-6):
-    coded, scaled = _norm_shapes(x, kind)
-    return (x.new_empty(x.shape if residual is not None else (0,)), x.new_empty(x.shape),
-            x.new_empty(coded, dtype=_KINDS.get(kind, torch.int8)),
+def _add_rms_norm_fake(x, weight, residual=None, kind="", eps=1e-6, normed=True):
+    summed, rows, coded, scaled = _norm_shapes(x, residual, kind, normed)
+    return (x.new_empty(summed), x.new_empty(rows), x.new_empty(coded, dtype=_KINDS.get(kind, torch.int8)),
             x.new_empty(scaled, dtype=torch.float32))
 
 

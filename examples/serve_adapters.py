@@ -97,7 +97,7 @@ def step(L, r, window, sinks):
                                      r.max_context, 1, window, sinks)
     shared = ops.scaled_linear(seen.view(T, nq), L.out)
     y = ops.lora_add(seen.view(T, nq), L.out_a, L.out_b, r.ids, base=shared, factors=L.factors)
-    total, _, codes2, scales2 = ops.add_rms_norm(y, L.norms[1], residual=r.stream, kind="fp8_block")
+    total, _, codes2, scales2 = ops.add_rms_norm(y, L.norms[1], residual=r.stream, kind="fp8_block", normed=False)
     up = ops.scaled_linear(codes2, L.up, scale_a=scales2, scale_b=L.up_scale, quant="block_fp8", act="silu")
     out = ops.scaled_linear(up, L.down, residual=total)
     return dict(stream=r.stream, x=x, codes=codes, scales=scales, plain=plain, qkv=qkv, turned=turned, seen=seen,
