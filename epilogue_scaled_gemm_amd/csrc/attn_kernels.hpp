@@ -38,8 +38,21 @@
 // like those of drafted nodes; the others run as without a window.
 //   48 sequences of up to 8191 positions in 8-bit codes, window 4096, take 79 us
 // (5.1 TB/s) and 5 for the join; 2 x 1500 nodes over 5001 positions, window 1024, 102
-// to 113 (0.5 PFLOP/s; two rounds of workgroups, the second half filled; bound by
-// vector instructions, about 190 for the 16 matrix instructions of a block).
+// to 113 (0.5 PFLOP/s).  Those are two rounds of workgroups, the second half filled;
+// matrix units are busy 22% of the cycles and vector units about a third (about 190
+// instructions for the 16 matrix instructions of a block), for the most part in
+// turns: neither bounds it alone.
+//
+// Weights.  Sums and statistics are in 32 bits, and l is of the unrounded weights, but
+// the weights of the second product are rounded to the rows' type, so that it takes one
+// matrix instruction and not two.  Relative to 64 bits (root mean square) the outputs are
+// off by 2.2 to 2.3e-3 in bf16 and 2.5 to 2.8e-4 in fp16, of which the result's own rounding
+// makes 1.66e-3 and 2.1e-4.  With what the rounding leaves out as a second part nothing
+// but that is left, at a price: 2 x 1500 nodes 122 us instead of 102, 2 x 700 of dim 256
+// 191 instead of 172, 48 sequences of 16-bit values 158 instead of 152, 24 of dim 256 222
+// instead of 180, small trees 16.7 instead of 16.3, 48 of codes 83.3 instead of 82.2; and as
+// second parts are zero or negative, infinite values would have to be looked for
+// everywhere.
 #pragma once
 
 #include <type_traits>

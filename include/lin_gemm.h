@@ -422,7 +422,8 @@ typedef struct {
  * Positions that no row sees are not read, but for those that share a block
  * of 128 with a visible one, whose values do not reach the result: page table
  * entries of dropped pages may hold anything.  Contexts may lie beyond the page
- * table, up to 2^31 - 2^23 positions. */
+ * table, up to 2^31 - 2^23 positions.  As in lin_gemm_tree_attention the
+ * probabilities are rounded to dtype for the product with the values. */
 int lin_gemm_window_attention(lin_gemm_t h, const lin_window_t *args, void *stream);
 
 typedef struct {
@@ -474,8 +475,9 @@ typedef struct {
 /* Root-mean-square norm of a decoder's stream, with the residual's addition
  * before it and the quantization that the next layer wants behind it:
  *   s = x + residual,  y = s / sqrt(mean(s^2) + eps) * weight
- * computed in binary32 (rows of any finite size).  residual_out = s and out =
- * y, rounded once; codes and scales as lin_gemm_quantize gives them, but of
+ * computed in binary32, eps too (rows of any finite size whose sum s binary32
+ * holds; beyond it s is an infinity).  residual_out = s and out = y, rounded
+ * once; codes and scales as lin_gemm_quantize gives them, but of
  * the unrounded y, so they go straight into lin_gemm_run (A and scales->a).
  * At least one of residual_out, out and codes is asked for.  Addresses and
  * row strides are multiples of 16 bytes; width is a multiple of 16 with codes
