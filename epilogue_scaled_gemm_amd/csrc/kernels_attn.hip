@@ -19,7 +19,7 @@ int64_t window_reach(int64_t window, int64_t sinks, int64_t nodes) { return sink
 // positions, window 1024: 256 rows whole 106 us, 128 rows 109 and in two splits 175;
 // window 4096: 288 and 285; 8 trees of 64 nodes: 61, 42 and 43; 200 nodes: 49, 34
 // and (128 rows in four splits) 28.  Dim 64, 2 x 1500 nodes: 85 and 82; dim 256,
-// 2 x 700: 94 whole, 77 in two splits.
+// 2 x 700: 176 and (two splits) 212, with 8 query and 2 key heads 89 and 73.
 AttnPlan window_plan(int64_t B, int Hk, int G, int D, int64_t max_nodes, int64_t max_len, int64_t all_rows,
                      int64_t window, int64_t sinks, bool masked) {
   AttnPlan best = {AT_TILE128, false, 1, 1, 128};
